@@ -10,9 +10,15 @@ library is not built, every call raises.
     out = kda.decode_step(q, k, v, log_alpha, beta, state)   # state updated in place
     # scalar-gate variants: Gated DeltaNet (log_alpha [B,T,H]) and DeltaNet (None)
     out, final_state = kda.gdn_forward(q, k, v, g, beta, initial_state)
+    # linear attention with one constant decay per head, and the paged-cache step of the
+    # softmax layers that stand between recurrent ones
+    out, final_state = kda.la_forward(q, k, v, log_decay, initial_state)
+    out = kda.la_decode_step(q, k, v, log_decay, state)
+    out = kda.paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -34,6 +40,9 @@ EXPORTS = ("kda_forward", "kda_forward_ws", "kda_forward_workspace_bytes",
            "kda_forward_host", "kda_forward_host_workspace_bytes",
            "kda_backward", "kda_backward_workspace_bytes",
            "kda_decode_step", "kda_gdn_forward", "kda_gdn_forward_ws", "kda_gdn_decode_step",
+           "kda_la_forward", "kda_la_forward_workspace_bytes", "kda_la_backward",
+           "kda_la_backward_workspace_bytes", "kda_la_decode_step",
+           "kda_paged_decode_step", "kda_paged_decode_workspace_bytes",
            "kda_status_string", "kda_check_status", "kda_selftest_timeout", "kda_last_cuda_error",
            "kda_launch_count",
            "kda_version")
@@ -99,6 +108,19 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kda_gdn_forward.argtypes = [vp] * 8 + [i] * 6 + [f, vp]
     lib.kda_gdn_decode_step.restype = i
     lib.kda_gdn_decode_step.argtypes = [vp] * 7 + [i] * 5 + [f, vp]
+    sz = ctypes.c_size_t
+    lib.kda_la_forward.restype = i
+    lib.kda_la_forward.argtypes = [vp] * 7 + [i] * 6 + [f, vp, sz, vp]
+    lib.kda_la_backward.restype = i
+    lib.kda_la_backward.argtypes = [vp] * 11 + [i] * 6 + [f, vp, sz, vp]
+    lib.kda_la_decode_step.restype = i
+    lib.kda_la_decode_step.argtypes = [vp] * 6 + [i] * 5 + [f, vp]
+    lib.kda_paged_decode_step.restype = i
+    lib.kda_paged_decode_step.argtypes = [vp] * 8 + [i] * 8 + [f, vp, sz, vp]
+    for name, n in (("kda_la_forward_workspace_bytes", 6), ("kda_la_backward_workspace_bytes", 6),
+                    ("kda_paged_decode_workspace_bytes", 4)):
+        getattr(lib, name).restype = sz
+        getattr(lib, name).argtypes = [i] * n
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [i]
     lib.kda_check_status.restype = i
@@ -132,6 +154,13 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _device(device: torch.device):
+    """Makes the tensors' device the current one for a launch, where it is not."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -554,6 +583,200 @@ def gdn_decode_step(q, k, v, log_alpha, beta, state, *, out=None, scale: float =
     """
     shape = None if log_alpha is None else (lambda B, H, dk: (B, H))
     return _decode("kda_gdn_decode_step", shape, q, k, v, log_alpha, beta, state, out, scale)
+
+
+def _la_workspace(fn, q, dk, dv, code, workspace, where):
+    """The workspace of a linear-attention call and its bytes: the caller's, or a new one
+    where the sizes need any (taken from torch's allocator on the current stream)."""
+    B, T, H = q.shape[:3]
+    if workspace is not None:
+        _need_workspace(workspace, q.device, where)
+        return workspace, workspace.numel() * workspace.element_size()
+    n = fn(B, T, H, dk, dv, code)
+    return (torch.empty(n, dtype=torch.uint8, device=q.device) if n else None), n
+
+
+def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, backward=False) -> int:
+    """Bytes of the workspace of :func:`la_forward` (or :func:`la_backward`); 0: none is needed."""
+    lib = load()
+    fn = lib.kda_la_backward_workspace_bytes if backward else lib.kda_la_forward_workspace_bytes
+    return int(fn(int(B), int(T), int(H), int(dk), int(dv), KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+
+
+def _need_la(q, k, v, log_decay, where):
+    """What the linear-attention calls check of their inputs; q's shape tells B, T and H."""
+    lead, dk, dev = tuple(q.shape[:-1]), q.shape[-1], q.device
+    _on_cuda(dev, where)
+    code = _dtype_code(q)
+    _need(q, "q", lead + (dk,), q.dtype, dev)
+    _need(k, "k", lead + (dk,), q.dtype, dev)
+    _need(v, "v", lead + (v.shape[-1],), q.dtype, dev)
+    if log_decay is not None:
+        _need(log_decay, "log_decay", (q.shape[-2],), torch.float32, dev)
+    return code
+
+
+def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=None,
+               return_final_state=True, scale: float = 0.0, workspace=None):
+    """Chunked prefill of linear attention with one decay per head (``kda_la_forward``).
+
+    ``S_t = exp(log_decay) S_{t-1} + k_t v_t^T``, ``o_t = scale S_t^T q_t``: q, k
+    ``[B,T,H,dk]`` and v ``[B,T,H,dv]`` (bf16 or fp32, one dtype); log_decay ``[H]`` fp32
+    (<= 0, a constant) or None (no decay); initial_state ``[B,H,dk,dv]`` fp32 or None.
+    Returns ``(out [B,T,H,dv] in the dtype of q, final_state [B,H,dk,dv] fp32 or None)``.
+    ``final_state`` may be ``initial_state`` (in-place carry).  ``scale`` 0 means
+    1/sqrt(dk).  ``workspace``: a uint8 device tensor of at least
+    :func:`la_workspace_bytes` bytes (allocated when None and needed).
+    """
+    lib = load()
+    code = _need_la(q, k, v, log_decay, "kda_la_forward")
+    B, T, H, dk = q.shape
+    dv, dev = v.shape[-1], q.device
+    if initial_state is not None:
+        _need(initial_state, "initial_state", (B, H, dk, dv), torch.float32, dev)
+    if out is None:
+        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", (B, T, H, dv), q.dtype, dev)
+    if final_state is not None:
+        _need(final_state, "final_state", (B, H, dk, dv), torch.float32, dev)
+    elif return_final_state:
+        final_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    ws, nbytes = _la_workspace(lib.kda_la_forward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_forward")
+    with _device(dev):
+        st = lib.kda_la_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(out),
+                                _ptr(final_state), B, T, H, dk, dv, code, float(scale), _ptr(ws), nbytes,
+                                _stream(dev))
+    _check(st, "kda_la_forward")
+    return out, final_state
+
+
+def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_state=None, *, workspace=None,
+                scale: float = 0.0, initial_state_grad: bool = True):
+    """Gradients of :func:`la_forward` (``kda_la_backward``).
+
+    ``grad_out`` [B,T,H,dv] in the dtype of q and ``grad_final_state`` [B,H,dk,dv] fp32
+    (None: zero) are the cotangents of the outputs and of the final state.  Returns a dict
+    ``dq, dk, dv`` (the dtype of q) and ``dinitial_state`` (fp32; None unless
+    ``initial_state_grad``).  ``log_decay`` is a constant: it has no gradient.
+    """
+    lib = load()
+    code = _need_la(q, k, v, log_decay, "kda_la_backward")
+    B, T, H, dk = q.shape
+    dv, dev = v.shape[-1], q.device
+    _need(grad_out, "grad_out", (B, T, H, dv), q.dtype, dev)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", (B, H, dk, dv), torch.float32, dev)
+    if grad_final_state is not None:
+        _need(grad_final_state, "grad_final_state", (B, H, dk, dv), torch.float32, dev)
+    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+             dinitial_state=torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+             if initial_state_grad else None)
+    ws, nbytes = _la_workspace(lib.kda_la_backward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_backward")
+    with _device(dev):
+        st = lib.kda_la_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(grad_out),
+                                 _ptr(grad_final_state), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
+                                 _ptr(g["dinitial_state"]), B, T, H, dk, dv, code, float(scale), _ptr(ws), nbytes,
+                                 _stream(dev))
+    _check(st, "kda_la_backward")
+    return g
+
+
+class LAFunction(torch.autograd.Function):
+    """``out, final_state = LAFunction.apply(q, k, v, log_decay, initial_state)`` with
+    ``kda_la_forward`` forward and ``kda_la_backward`` backward.  ``log_decay`` is a
+    constant of the layer: it must not require a gradient."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, initial_state):
+        if log_decay is not None and log_decay.requires_grad:
+            raise ValueError("log_decay is a constant: kda_la_backward returns no gradient for it")
+        out, final_state = la_forward(q, k, v, log_decay, initial_state)
+        ctx.save_for_backward(q, k, v, log_decay, initial_state)
+        return out, final_state
+
+    @staticmethod
+    def backward(ctx, grad_out, grad_final_state):
+        q, k, v, log_decay, initial_state = ctx.saved_tensors
+        g = la_backward(q, k, v, log_decay, grad_out.contiguous(), initial_state,
+                        None if grad_final_state is None else grad_final_state.contiguous(),
+                        initial_state_grad=initial_state is not None)
+        return g["dq"], g["dk"], g["dv"], None, g["dinitial_state"]
+
+
+def la_decode_step(q, k, v, log_decay, state, *, out=None, scale: float = 0.0):
+    """One token per sequence of :func:`la_forward` (``kda_la_decode_step``); ``state`` is
+    updated in place.
+
+    q, k ``[B,H,dk]``, v ``[B,H,dv]`` (bf16 or fp32); log_decay ``[H]`` fp32 or None; state
+    ``[B,H,dk,dv]`` fp32.  Returns ``out [B,H,dv]`` in the dtype of q.
+    """
+    lib = load()
+    code = _need_la(q, k, v, log_decay, "kda_la_decode_step")
+    B, H, dk = q.shape
+    dv, dev = v.shape[-1], q.device
+    _need(state, "state", (B, H, dk, dv), torch.float32, dev)
+    if out is None:
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", (B, H, dv), q.dtype, dev)
+    with _device(dev):
+        st = lib.kda_la_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(out), B, H, dk, dv,
+                                    code, float(scale), _stream(dev))
+    _check(st, "kda_la_decode_step")
+    return out
+
+
+def paged_decode_workspace_bytes(H: int, Hkv: int, D: int, dtype=torch.bfloat16) -> int:
+    """Bytes of the workspace of :func:`paged_decode_step`, whatever the batch and lengths."""
+    return int(load().kda_paged_decode_workspace_bytes(int(H), int(Hkv), int(D),
+                                                       KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+
+
+def paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths, *, out=None, scale: float = 0.0,
+                      workspace=None):
+    """One token per sequence of a softmax-attention layer on a paged key-value cache
+    (``kda_paged_decode_step``); the caches are updated in place.
+
+    q ``[B,H,D]``, k, v ``[B,Hkv,D]`` (or both None: attend to what the cache holds), k_cache,
+    v_cache ``[num_pages,page_size,Hkv,D]``, all bf16 or fp32; block_table ``[B,max_pages]``
+    int32; lengths ``[B]`` int32, the keys in the cache before the call (not changed;
+    negative: an idle row, which keeps its row of ``out``).  Returns ``out [B,H,D]`` in the
+    dtype of q.  A prompt enters the cache by indexing: position t of row b is
+    ``k_cache[block_table[b, t // page_size], t % page_size]``.
+    """
+    lib = load()
+    B, H, D = q.shape
+    num_pages, page_size, Hkv = k_cache.shape[:3]
+    max_pages = block_table.shape[-1]
+    dev = q.device
+    _on_cuda(dev, "kda_paged_decode_step")
+    code = _dtype_code(q)
+    _need(q, "q", (B, H, D), q.dtype, dev)
+    if (k is None) != (v is None):
+        raise ValueError("kda_paged_decode_step: k and v are given together or not at all")
+    if k is not None:
+        _need(k, "k", (B, Hkv, D), q.dtype, dev)
+        _need(v, "v", (B, Hkv, D), q.dtype, dev)
+    _need(k_cache, "k_cache", (num_pages, page_size, Hkv, D), q.dtype, dev)
+    _need(v_cache, "v_cache", (num_pages, page_size, Hkv, D), q.dtype, dev)
+    _need(block_table, "block_table", (B, max_pages), torch.int32, dev)
+    _need(lengths, "lengths", (B,), torch.int32, dev)
+    if out is None:
+        out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
+    else:
+        _need(out, "out", (B, H, D), q.dtype, dev)
+    if workspace is None:
+        workspace = torch.empty(lib.kda_paged_decode_workspace_bytes(H, Hkv, D, code), dtype=torch.uint8, device=dev)
+    else:
+        _need_workspace(workspace, dev, "kda_paged_decode_step")
+    with _device(dev):
+        st = lib.kda_paged_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                       _ptr(lengths), _ptr(out), B, H, Hkv, D, num_pages, page_size, max_pages, code,
+                                       float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _stream(dev))
+    _check(st, "kda_paged_decode_step")
+    return out
 
 
 def check_status(device=None):

@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include "kda_internal.cuh"
+#include "kda_paged.cuh"
 
 namespace {
 
@@ -80,6 +81,8 @@ cudaError_t device_pool(bool create, cudaMemPool_t *out)
 }  // namespace
 
 void kda::note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+void kda::clear_cuda_error() { g_last_cuda_error[0] = '\0'; }
+kda_status kda::record_cuda_error(cudaError_t e) { return cuda_fail(e); }
 
 extern "C" {
 
@@ -677,12 +680,14 @@ kda_status kda_check_status(void *stream)
     g_last_cuda_error[0] = '\0';
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned int dev_status = 0, gdn_status = 0, split_status = 0;
+    unsigned int dev_status = 0, gdn_status = 0, split_status = 0, paged_status = 0;
     e = kda::take_device_status(&dev_status);
     if (e == cudaSuccess) e = kda::take_gdn_device_status(&gdn_status);
     if (e == cudaSuccess) e = kda::take_split_device_status(&split_status);
+    if (e == cudaSuccess) e = kda::take_paged_device_status(&paged_status);
     if (e != cudaSuccess) return cuda_fail(e);
-    return (dev_status | gdn_status | split_status) ? KDA_ERR_TIMEOUT : KDA_OK;
+    if (dev_status | gdn_status | split_status) return KDA_ERR_TIMEOUT;
+    return paged_status ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 
 }  // extern "C"

@@ -108,6 +108,11 @@ cudaError_t take_device_status(unsigned int *status);
 // Counts one kernel enqueued through the library (see kda_launch_count).
 void note_launch();
 
+// kda_last_cuda_error of this thread: cleared at the start of a call, set by the first
+// failure (returns KDA_ERR_CUDA).
+void clear_cuda_error();
+kda_status record_cuda_error(cudaError_t e);
+
 // Loads of the two input dtypes as fp32 (bf16 -> fp32 is exact).
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

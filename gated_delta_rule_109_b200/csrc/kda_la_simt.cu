@@ -1,0 +1,333 @@
+// Linear attention with one decay per head on CUDA cores, fp32 arithmetic throughout
+// (the mathematics is in kda_la.cuh).
+//
+// One CTA walks the chunks of 64 tokens of one (pass, b, h, segment) with the state
+// resident in shared memory.  A chunk is four small products of register tiles:
+// 64 x 64 scores (4 x 4 a thread), the outputs P V + Q S (4 rows x DV/16 columns a
+// thread) and the state K'^T V (DK/16 x DV/16 a thread), operands read as 16-byte
+// vectors of padded rows.  Powers of lambda are computed in 64 bits once per CTA, so
+// their rounding does not grow along the sequence.
+#include "kda_la.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kC = 64;
+constexpr int kThreads = 256;
+
+template <int DK, int DV>
+struct LaSmem {
+    static constexpr int PK = DK + 4, PV = DV + 4, PP = kC + 4;   // row pitches: 16-byte aligned, 4 banks apart
+    static constexpr int off_q = 0;
+    static constexpr int off_k = off_q + kC * PK;
+    static constexpr int off_v = off_k + kC * PK;
+    static constexpr int off_p = off_v + kC * PV;
+    static constexpr int off_s = off_p + kC * PP;
+    static constexpr int off_w = off_s + DK * PV;                 // lambda^n, n = 0..64
+    static constexpr int total = off_w + kC + 4;
+    static constexpr size_t bytes = sizeof(float) * (size_t)total;
+};
+
+__device__ __forceinline__ void fma4(float4 &acc, float a, float4 b)
+{
+    acc.x += a * b.x; acc.y += a * b.y; acc.z += a * b.z; acc.w += a * b.w;
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b, float acc)
+{
+    acc += a.x * b.x; acc += a.y * b.y; acc += a.z * b.z; acc += a.w * b.w;
+    return acc;
+}
+
+template <int DK, int DV, typename InT, bool STATES_ONLY>
+__global__ void __launch_bounds__(kThreads, 1)
+la_simt_kernel(const __grid_constant__ LaArgs a)
+{
+    using L = LaSmem<DK, DV>;
+    constexpr int PK = L::PK, PV = L::PV, PP = L::PP;
+    constexpr int RK = DK / 16, CV = DV / 64;   // state rows, float4 column groups per thread
+    extern __shared__ __align__(16) float sm[];
+    float *sQ = sm + L::off_q, *sK = sm + L::off_k, *sV = sm + L::off_v, *sP = sm + L::off_p, *sS = sm + L::off_s;
+    float *sW = sm + L::off_w;
+
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
+    const int seg = blockIdx.x % nwork;
+    const int bh = (blockIdx.x / nwork) % (a.B * a.H);
+    const int ip = blockIdx.x / nwork / (a.B * a.H);
+    const LaPass &ps = a.pass[ip];
+    const int b = bh / a.H, h = bh % a.H, rev = ps.rev;
+    int t_lo, t_hi;
+    la_segment(seg, a.nseg, a.seg_tokens, a.T, rev, t_lo, t_hi);
+    float *slots = a.nseg > 1 ? a.ws + ((size_t)ip * a.B * a.H + bh) * a.nseg * DK * DV : nullptr;
+
+    if (tid <= kC) sW[tid] = (float)la_power(a.log_decay, h, tid);
+    // ---- entering state
+    if (STATES_ONLY) {
+        for (int e = tid; e < DK * DV; e += kThreads) sS[(e / DV) * PV + e % DV] = 0.f;
+    } else {
+        const float *s0 = slots ? slots + (size_t)seg * DK * DV : ps.s0 ? ps.s0 + (size_t)bh * DK * DV : nullptr;
+        const bool tr = !slots && ps.s0_transposed;
+        for (int e = tid; e < DK * DV; e += kThreads) {
+            const int r = e / DV, c = e % DV;
+            sS[r * PV + c] = s0 ? s0[tr ? c * DK + r : e] : 0.f;
+        }
+    }
+
+    const InT *q = static_cast<const InT *>(ps.q), *k = static_cast<const InT *>(ps.k), *v = static_cast<const InT *>(ps.v);
+    const int n0 = t_lo / kC, n1 = (t_hi + kC - 1) / kC;
+    for (int it = n0; it < n1; ++it) {
+        const int n = rev ? n1 - 1 - (it - n0) : it;
+        const int t0 = n * kC, c = min(kC, t_hi - t0);
+        __syncthreads();                        // the chunk before is consumed
+        // ---- stage q, k, v (rows past c are zero: they change nothing)
+        for (int e = tid; e < kC * DK / 4; e += kThreads) {
+            const int t = e / (DK / 4), x = 4 * (e % (DK / 4));
+            const size_t g = (((size_t)b * a.T + t0 + t) * a.H + h) * DK + x;
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!STATES_ONLY) la_store4(sQ + t * PK + x, t < c ? la_load4(q + g) : z);
+            la_store4(sK + t * PK + x, t < c ? la_load4(k + g) : z);
+        }
+        for (int e = tid; e < kC * DV / 4; e += kThreads) {
+            const int t = e / (DV / 4), x = 4 * (e % (DV / 4));
+            const size_t g = (((size_t)b * a.T + t0 + t) * a.H + h) * DV + x;
+            la_store4(sV + t * PV + x, t < c ? la_load4(v + g) : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+        __syncthreads();
+
+        if (!STATES_ONLY) {
+            // ---- P_ij = f_intra lambda^|i-j| (q_i . k_j) on the causal side; rows ty + 16 a, columns tx + 16 b
+            float s[4][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < DK; d += 4) {
+                float4 x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = la_load4(sQ + (ty + 16 * i) * PK + d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = la_load4(sK + (tx + 16 * j) * PK + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = ty + 16 * i, m = tx + 16 * j, ahead = rev ? m - r : r - m;
+                    sP[r * PP + m] = ahead >= 0 ? s[i][j] * (sW[max(ahead, 0)] * ps.f_intra) : 0.f;
+                }
+            __syncthreads();
+            // ---- out rows ty + 16 a, columns 4 tx + 64 b: P V + lambda^(.) Q S
+            float4 o[4][CV], x[4][CV];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int m = 0; m < CV; ++m) o[i][m] = x[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int j = 0; j < kC; j += 4) {
+                float4 p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = la_load4(sP + (ty + 16 * i) * PP + j);
+#pragma unroll
+                for (int m = 0; m < CV; ++m)
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        const float4 y = la_load4(sV + (j + jj) * PV + 4 * tx + 64 * m);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            fma4(o[i][m], jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w, y);
+                    }
+            }
+#pragma unroll 2
+            for (int d = 0; d < DK; d += 4) {
+                float4 p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = la_load4(sQ + (ty + 16 * i) * PK + d);
+#pragma unroll
+                for (int m = 0; m < CV; ++m)
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        const float4 y = la_load4(sS + (d + jj) * PV + 4 * tx + 64 * m);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            fma4(x[i][m], jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w, y);
+                    }
+            }
+            InT *out = static_cast<InT *>(ps.out);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = ty + 16 * i;
+                if (r >= c) continue;
+                const float f = ps.f_inter * sW[rev ? c - 1 - r : r + 1];
+                const size_t g = (((size_t)b * a.T + t0 + r) * a.H + h) * DV + 4 * tx;
+#pragma unroll
+                for (int m = 0; m < CV; ++m) {
+                    fma4(o[i][m], f, x[i][m]);
+                    la_store4(out + g + 64 * m, o[i][m]);
+                }
+            }
+            __syncthreads();                    // every reader of the state and of k is done
+        }
+        // ---- k_j <- f_write lambda^(.) k_j, then S <- lambda^c S + K'^T V
+        for (int e = tid; e < kC * DK; e += kThreads) {
+            const int t = e / DK;
+            if (t < c) sK[t * PK + e % DK] *= ps.f_write * sW[rev ? t + 1 : c - 1 - t];
+        }
+        __syncthreads();
+        float4 u[RK][CV];
+#pragma unroll
+        for (int r = 0; r < RK; ++r)
+#pragma unroll
+            for (int m = 0; m < CV; ++m) u[r][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // rows 4 ty + 64 r4 + {0..3}: RK = 4 or 8 rows in RK / 4 groups
+#pragma unroll 2
+        for (int j = 0; j < kC; ++j) {
+            float4 y[CV];
+#pragma unroll
+            for (int m = 0; m < CV; ++m) y[m] = la_load4(sV + j * PV + 4 * tx + 64 * m);
+#pragma unroll
+            for (int g = 0; g < RK / 4; ++g) {
+                const float4 x = la_load4(sK + j * PK + 4 * ty + 64 * g);
+#pragma unroll
+                for (int m = 0; m < CV; ++m) {
+                    fma4(u[4 * g][m], x.x, y[m]);
+                    fma4(u[4 * g + 1][m], x.y, y[m]);
+                    fma4(u[4 * g + 2][m], x.z, y[m]);
+                    fma4(u[4 * g + 3][m], x.w, y[m]);
+                }
+            }
+        }
+        const double lc = la_power(a.log_decay, h, c);
+        const float hi = (float)lc, lo = (float)(lc - (double)hi);
+#pragma unroll
+        for (int r = 0; r < RK; ++r)
+#pragma unroll
+            for (int m = 0; m < CV; ++m) {
+                float *p = sS + (4 * ty + 64 * (r / 4) + r % 4) * PV + 4 * tx + 64 * m;
+                const float4 s = la_load4(p);
+                fma4(u[r][m], lo, s);
+                fma4(u[r][m], hi, s);
+                la_store4(p, u[r][m]);
+            }
+    }
+    __syncthreads();
+    // ---- leaving state
+    float *dst = STATES_ONLY ? slots + (size_t)(seg + 1) * DK * DV
+                 : (seg == a.nseg - 1 && ps.sT) ? ps.sT + (size_t)bh * DK * DV : nullptr;
+    if (dst)
+        for (int e = tid; e < DK * DV; e += kThreads) dst[e] = sS[(e / DV) * PV + e % DV];
+}
+
+template <int DK, int DV, typename InT, bool STATES_ONLY>
+cudaError_t launch_typed(const LaArgs &a, cudaStream_t stream)
+{
+    auto kernel = la_simt_kernel<DK, DV, InT, STATES_ONLY>;
+    constexpr size_t bytes = LaSmem<DK, DV>::bytes;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
+    kernel<<<(unsigned)((size_t)a.npass * a.B * a.H * nwork), kThreads, bytes, stream>>>(a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) note_launch();
+    return e;
+}
+
+template <typename InT, bool STATES_ONLY>
+cudaError_t launch_dims(const LaArgs &a, cudaStream_t stream)
+{
+    if (a.dk == 128 && a.dv == 128) return launch_typed<128, 128, InT, STATES_ONLY>(a, stream);
+    if (a.dk == 64 && a.dv == 64) return launch_typed<64, 64, InT, STATES_ONLY>(a, stream);
+    if (a.dk == 128 && a.dv == 64) return launch_typed<128, 64, InT, STATES_ONLY>(a, stream);
+    if (a.dk == 64 && a.dv == 128) return launch_typed<64, 128, InT, STATES_ONLY>(a, stream);
+    return cudaErrorInvalidValue;
+}
+
+// Slot s of a (pass, b, h) holds segment s - 1's own state (slot 0: nothing); afterwards
+// it holds the state that enters segment s: S_0 the pass's initial state, then
+// S_s = lambda^(tokens of segment s - 1) S_{s-1} + slot s.  One thread per four elements.
+__global__ void __launch_bounds__(256)
+la_scan_kernel(const __grid_constant__ LaArgs a)
+{
+    const int quads = a.dk * a.dv / 4;
+    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t head = id / quads;
+    const int e = 4 * (int)(id % quads);
+    const int nbh = a.B * a.H;
+    if (head >= (size_t)a.npass * nbh) return;
+    const int ip = (int)(head / nbh), bh = (int)(head % nbh);
+    const LaPass &ps = a.pass[ip];
+    float *slot = a.ws + head * a.nseg * a.dk * a.dv + e;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ps.s0) {
+        const float *s0 = ps.s0 + (size_t)bh * a.dk * a.dv;
+        if (ps.s0_transposed) {
+            const float *p = s0 + (e % a.dv) * a.dk + e / a.dv;
+            s = make_float4(p[0], p[a.dk], p[2 * a.dk], p[3 * a.dk]);
+        } else s = *reinterpret_cast<const float4 *>(s0 + e);
+    }
+    *reinterpret_cast<float4 *>(slot) = s;
+    for (int g = 1; g < a.nseg; ++g) {
+        int t0, t1;
+        la_segment(g - 1, a.nseg, a.seg_tokens, a.T, ps.rev, t0, t1);
+        const double l = la_power(a.log_decay, bh % a.H, t1 - t0);
+        const float hi = (float)l, lo = (float)(l - (double)hi);
+        float *p = slot + (size_t)g * a.dk * a.dv;
+        float4 u = *reinterpret_cast<const float4 *>(p);
+        fma4(u, lo, s);
+        fma4(u, hi, s);
+        *reinterpret_cast<float4 *>(p) = s = u;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t stream)
+{
+    if (a.dtype == KDA_BF16)
+        return states_only ? launch_dims<__nv_bfloat16, true>(a, stream) : launch_dims<__nv_bfloat16, false>(a, stream);
+    return states_only ? launch_dims<float, true>(a, stream) : launch_dims<float, false>(a, stream);
+}
+
+int la_chunk(int, int, kda_dtype) { return kC; }
+
+// Segments: with one per head the outputs' launch has npass B H CTAs that walk all chunks;
+// with n of them the walk is n times shorter, but every segment's state has to be known
+// first (a second walk over k and v) and joined.  The number with the least modelled time is
+// taken: waves of CTAs x chunks of a walk, the state walk at a fraction of the output walk's
+// cost per chunk, and a fixed cost (in chunks) for the two further launches.
+void la_choose_segments(LaArgs &a)
+{
+    constexpr int kSms = 148, kMaxSegments = 64;
+    constexpr double kStateCost = 0.5, kJoinCost = 2.0;
+    const int C = la_chunk(a.dk, a.dv, a.dtype);
+    const int chunks = (a.T + C - 1) / C;
+    const long long heads = (long long)a.npass * a.B * a.H;
+    a.nseg = 1;
+    a.seg_tokens = a.T > 0 ? chunks * C : C;
+    double best = 0.0;
+    for (int want = 1; want <= kMaxSegments && want <= chunks; ++want) {
+        const int len = (chunks + want - 1) / want, n = (chunks + len - 1) / len;
+        const long long out_waves = (heads * n + kSms - 1) / kSms, state_waves = (heads * (n - 1) + kSms - 1) / kSms;
+        const double t = (double)out_waves * len + (n > 1 ? kStateCost * state_waves * len + kJoinCost : 0.0);
+        if (want == 1 || t < best) {
+            best = t;
+            a.nseg = n;
+            a.seg_tokens = len * C;
+        }
+    }
+}
+
+cudaError_t launch_la(const LaArgs &a, cudaStream_t stream)
+{
+    if (a.nseg > 1) {
+        cudaError_t e = launch_la_simt(a, true, stream);
+        if (e != cudaSuccess) return e;
+        const size_t n = (size_t)a.npass * a.B * a.H * (a.dk * a.dv / 4);
+        la_scan_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        note_launch();
+    }
+    return launch_la_simt(a, false, stream);
+}
+
+}  // namespace kda

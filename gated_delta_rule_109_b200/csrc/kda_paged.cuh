@@ -1,0 +1,43 @@
+// Attention of one new token per sequence over a paged key-value cache: declarations and
+// the split of the work shared by its kernels (internal header).
+//
+//     o = softmax(scale q K^T) V
+// over the keys and values that a sequence's pages hold, the new token's own included when
+// the call carries them (they are written to the cache as well).  Query heads h of one
+// group h / (H / Hkv) share a key-value head.
+//
+// Split: a unit is kPagedTile consecutive keys of one (sequence, key-value head, block of
+// query heads), and all units lie on one line ordered by those three.  Of the U units CTA c of
+// G (at most U of them) takes [c U / G, (c + 1) U / G), whatever sequence they belong to, so
+// the CTAs' shares differ by at most one unit for every mix of lengths.  A stretch of units
+// with one owner is written out at once; one that several CTAs share leaves each owner's
+// running maximum, sum and unnormalised output in the workspace, and a second kernel joins
+// them.  The lengths are read on the device: nothing of the split depends on what the host
+// knows.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+constexpr int kPagedTile = 64;
+
+struct PagedArgs {
+    const void *q, *k, *v;          // [B, H, D], [B, Hkv, D] or null, ditto
+    void *k_cache, *v_cache;        // [num_pages, page_size, Hkv, D]
+    const int *block_table;         // [B, max_pages]
+    const int *lengths;             // [B] keys in the cache before the call; negative: idle row
+    void *out;                      // [B, H, D]
+    int B, H, Hkv, D, num_pages, page_size, max_pages;
+    kda_dtype dtype;
+    float scale;
+    float *ws;
+};
+
+size_t paged_workspace_bytes(int H, int Hkv, int D, kda_dtype dtype);
+cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t stream);
+// Reads and clears the status word: bit 0: a row named a page outside the cache or a length
+// beyond its table.  Synchronous.
+cudaError_t take_paged_device_status(unsigned int *status);
+
+}  // namespace kda

@@ -41,7 +41,8 @@
  * - Calls never throw and never abort; they are safe to call from several
  *   host threads on different streams.
  * - Outputs are fp32 for both input dtypes (bf16 output would already exceed
- *   the 2e-3 relative error the bf16 path is held to).
+ *   the 2e-3 relative error the bf16 path is held to).  The linear-attention and
+ *   paged calls (kda_la_*, kda_paged_*) return the dtype of their inputs.
  */
 #ifndef KDA_H
 #define KDA_H
@@ -462,14 +463,140 @@ kda_status kda_backward(const void *q, const void *k, const void *v,
  * dk * dv * 4 (0 for unsupported shapes). */
 size_t kda_backward_workspace_bytes(int B, int T, int H, int dk, int dv);
 
+/*
+ * kda_la_forward -- chunked prefill of linear attention with one decay per head.
+ *
+ * The family's member without the delta rule: every token decays the state by its
+ * head's constant lambda = exp(log_decay) and adds its key-value product,
+ *
+ *     S_t = lambda S_{t-1} + k_t v_t^T,    o_t = scale * S_t^T q_t
+ *
+ * ("Kimi Delta Attention: The Linear Attention Behind Kimi K2 and Qwen3", the
+ * linear-attention step S += v k^T, o = S q, with a forgetting factor).
+ *
+ *   q, k          [B, T, H, dk]  dtype            (16-byte aligned)
+ *   v             [B, T, H, dv]  dtype            (16-byte aligned)
+ *   log_decay     [H]            float32 or NULL  (4-byte aligned; NULL = lambda 1): <= 0,
+ *                 -inf (lambda = 0) included.  A constant: no call returns its gradient.
+ *   initial_state [B, H, dk, dv] float32 or NULL  (16-byte aligned; NULL = zero state)
+ *   out           [B, T, H, dv]  dtype            (16-byte aligned)
+ *   final_state   [B, H, dk, dv] float32 or NULL  (16-byte aligned; NULL = not written)
+ *   workspace     device buffer of kda_la_forward_workspace_bytes(...) bytes (256-byte
+ *                 aligned, caller-owned; NULL where that is 0): the states at which the
+ *                 sequence is cut so that few heads fill the device.  Not to be used by
+ *                 another call that may run at the same time.
+ *
+ * Unlike kda_forward's, `out` has the dtype of q: the products of 16-bit inputs are
+ * summed in fp32 and rounded once.  The state is fp32 throughout.  final_state may be
+ * initial_state (in-place carry); any other overlap of inputs and outputs is undefined.
+ * q and k need not be normalised.  Inputs are finite: an infinity or NaN in a token may
+ * reach the outputs of earlier tokens of its chunk (128 tokens).
+ *
+ * Supported: dk, dv in {64, 128}, both dtypes; bf16 with dk = dv = 128 runs on the
+ * tensor cores, anything else in fp32 on CUDA cores.  B, H >= 1, T >= 0; T = 0 writes no
+ * output and sets final_state to initial_state (or zeros).  A workspace that is missing
+ * or too small: KDA_ERR_INVALID_ARG; misaligned: KDA_ERR_MISALIGNED.  Asynchronous on
+ * `stream`; deterministic; may be captured into a graph.
+ */
+kda_status kda_la_forward(const void *q, const void *k, const void *v, const float *log_decay,
+                          const float *initial_state, void *out, float *final_state,
+                          int B, int T, int H, int dk, int dv, kda_dtype dtype, float scale,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * kda_la_backward -- gradients of kda_la_forward for q, k, v and initial_state.
+ *
+ * With the loss L = sum(out * grad_out) + sum(final_state * grad_final_state):
+ *
+ *   grad_out         [B, T, H, dv]  dtype   (16-byte aligned)  dL/d out
+ *   grad_final_state [B, H, dk, dv] float32 (16-byte aligned) or NULL (zero)
+ *   grad_q, grad_k   [B, T, H, dk], grad_v [B, T, H, dv]  dtype, overwritten (16-byte aligned)
+ *   grad_initial_state [B, H, dk, dv] float32 output (16-byte aligned) or NULL (not wanted)
+ *   workspace        device buffer of kda_la_backward_workspace_bytes(...) bytes
+ *                    (256-byte aligned, caller-owned; NULL where that is 0)
+ *
+ * Everything else as for kda_la_forward.  The outputs may not alias the inputs.  T = 0
+ * writes grad_initial_state = grad_final_state (or zeros) and nothing else.
+ */
+kda_status kda_la_backward(const void *q, const void *k, const void *v, const float *log_decay,
+                           const float *initial_state, const void *grad_out, const float *grad_final_state,
+                           void *grad_q, void *grad_k, void *grad_v, float *grad_initial_state,
+                           int B, int T, int H, int dk, int dv, kda_dtype dtype, float scale,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of kda_la_forward and kda_la_backward; 0 where none is needed (and for
+ * sizes or types that the calls refuse). */
+size_t kda_la_forward_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype dtype);
+size_t kda_la_backward_workspace_bytes(int B, int T, int H, int dk, int dv, kda_dtype dtype);
+
+/*
+ * kda_la_decode_step -- one token per sequence of kda_la_forward, state updated in place.
+ *
+ *   q, k [B, H, dk], v [B, H, dv], out [B, H, dv]  dtype; log_decay [H] float32 or NULL;
+ *   state_inout [B, H, dk, dv] float32, read and overwritten.  Alignments as above.
+ *
+ * Equivalent to kda_la_forward with T = 1 and final_state == initial_state.
+ */
+kda_status kda_la_decode_step(const void *q, const void *k, const void *v, const float *log_decay,
+                              float *state_inout, void *out, int B, int H, int dk, int dv,
+                              kda_dtype dtype, float scale, void *stream);
+
+/*
+ * kda_paged_decode_step -- one token per sequence of a softmax-attention layer whose state
+ * is a paged key-value cache, updated in place.
+ *
+ * The other layer of a hybrid stack ("KDA Technical Deep Dive" describes models that mix
+ * recurrent layers with full attention and serve both kinds of state).  Row b holds
+ * lengths[b] keys; its new key and value are written to position lengths[b] and
+ *
+ *     out = softmax(scale * q K^T) V
+ *
+ * is taken over the lengths[b] + 1 keys.  Query head h reads key-value head h / (H / Hkv).
+ *
+ *   q             [B, H, D]      dtype   (16-byte aligned)
+ *   k, v          [B, Hkv, D]    dtype   (16-byte aligned), or both NULL: nothing is written
+ *                 and the row attends to the lengths[b] keys that are there
+ *   k_cache, v_cache [num_pages, page_size, Hkv, D] dtype (16-byte aligned)
+ *   block_table   [B, max_pages] int32   (4-byte aligned): position t of row b is entry
+ *                 t % page_size of page block_table[b][t / page_size].  Entries behind the
+ *                 last position in use are not read.
+ *   lengths       [B]            int32   (4-byte aligned); not changed by the call
+ *   out           [B, H, D]      dtype   (16-byte aligned)
+ *   workspace     device buffer of kda_paged_decode_workspace_bytes(H, Hkv, D, dtype) bytes
+ *                 (256-byte aligned, caller-owned), whatever the batch and the lengths; not
+ *                 to be used by another call that may run at the same time
+ *
+ * A row with lengths[b] < 0 is idle: its cache and its row of out are left as they were.  A
+ * row without keys (k = v = NULL, lengths[b] = 0) gets zeros.  Rows may share pages that
+ * they only read; two rows that write the same position leave one of the two there.
+ * Memory of the cache behind a row's last key is never used, whatever it holds.  Lengths
+ * and pages are read on the device.  A page outside [0, num_pages) counts as absent (its
+ * keys weigh nothing, a key for it is not stored), a row longer than its table is left as
+ * an idle one, and the next kda_check_status returns KDA_ERR_INVALID_ARG for either.
+ *
+ * Scores, maximum, sum and output are fp32; out is rounded once.  D in {64, 128}, any
+ * page_size >= 1, H a multiple of Hkv, max_pages * page_size < 2^31 - 1024, both dtypes.
+ * Asynchronous on `stream`; deterministic; may be captured into a graph and replayed with
+ * other lengths, pages and data.
+ */
+kda_status kda_paged_decode_step(const void *q, const void *k, const void *v, void *k_cache, void *v_cache,
+                                 const int *block_table, const int *lengths, void *out,
+                                 int B, int H, int Hkv, int D, int num_pages, int page_size, int max_pages,
+                                 kda_dtype dtype, float scale, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Workspace bytes of kda_paged_decode_step (0 for arguments that it refuses). */
+size_t kda_paged_decode_workspace_bytes(int H, int Hkv, int D, kda_dtype dtype);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char *kda_status_string(kda_status status);
 
 /*
  * kda_check_status -- synchronise `stream`, then report (and clear) any
  * device-side failure the library's kernels recorded on the current device:
- * KDA_ERR_TIMEOUT if a bounded wait gave up, KDA_ERR_CUDA if the stream
- * reports an error, else KDA_OK.
+ * KDA_ERR_TIMEOUT if a bounded wait gave up, KDA_ERR_INVALID_ARG if a
+ * kda_paged_decode_step met a page or a length outside its cache, KDA_ERR_CUDA if
+ * the stream reports an error, else KDA_OK.
  */
 kda_status kda_check_status(void *stream);
 
