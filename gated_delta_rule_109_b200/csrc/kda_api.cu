@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include "kda_internal.cuh"
+#include "kda_la.cuh"
 #include "kda_paged.cuh"
 
 namespace {
@@ -680,13 +681,14 @@ kda_status kda_check_status(void *stream)
     g_last_cuda_error[0] = '\0';
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e);
-    unsigned int dev_status = 0, gdn_status = 0, split_status = 0, paged_status = 0;
+    unsigned int dev_status = 0, gdn_status = 0, split_status = 0, la_status = 0, paged_status = 0;
     e = kda::take_device_status(&dev_status);
     if (e == cudaSuccess) e = kda::take_gdn_device_status(&gdn_status);
     if (e == cudaSuccess) e = kda::take_split_device_status(&split_status);
+    if (e == cudaSuccess) e = kda::take_la_device_status(&la_status);
     if (e == cudaSuccess) e = kda::take_paged_device_status(&paged_status);
     if (e != cudaSuccess) return cuda_fail(e);
-    if (dev_status | gdn_status | split_status) return KDA_ERR_TIMEOUT;
+    if (dev_status | gdn_status | split_status | la_status) return KDA_ERR_TIMEOUT;
     return paged_status ? KDA_ERR_INVALID_ARG : KDA_OK;
 }
 

@@ -61,6 +61,12 @@ cudaError_t launch_la(const LaArgs &a, cudaStream_t stream);
 // states_only: each segment's state from zero goes to its slot of a.ws, no outputs.
 cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t stream);
 
+// Tensor cores (tcgen05): bf16 with dk = dv = 128.
+bool la_tc_supported(int dk, int dv, kda_dtype dtype);
+cudaError_t launch_la_tc(const LaArgs &a, bool states_only, cudaStream_t stream);
+// Reads and clears the status word that the kernel sets when a bounded wait gives up.  Synchronous.
+cudaError_t take_la_device_status(unsigned int *status);
+
 struct LaDecodeArgs {
     const void *q, *k, *v;
     const float *log_decay;     // [H] or null

@@ -288,7 +288,7 @@ cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t strea
     return states_only ? launch_dims<float, true>(a, stream) : launch_dims<float, false>(a, stream);
 }
 
-int la_chunk(int, int, kda_dtype) { return kC; }
+int la_chunk(int dk, int dv, kda_dtype dtype) { return la_tc_supported(dk, dv, dtype) ? 128 : kC; }
 
 // Segments: with one per head the outputs' launch has npass B H CTAs that walk all chunks;
 // with n of them the walk is n times shorter, but every segment's state has to be known
@@ -319,15 +319,16 @@ void la_choose_segments(LaArgs &a)
 
 cudaError_t launch_la(const LaArgs &a, cudaStream_t stream)
 {
+    const auto launch = la_tc_supported(a.dk, a.dv, a.dtype) ? launch_la_tc : launch_la_simt;
     if (a.nseg > 1) {
-        cudaError_t e = launch_la_simt(a, true, stream);
+        cudaError_t e = launch(a, true, stream);
         if (e != cudaSuccess) return e;
         const size_t n = (size_t)a.npass * a.B * a.H * (a.dk * a.dv / 4);
         la_scan_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         note_launch();
     }
-    return launch_la_simt(a, false, stream);
+    return launch(a, false, stream);
 }
 
 }  // namespace kda
