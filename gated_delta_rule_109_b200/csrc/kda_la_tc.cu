@@ -14,8 +14,10 @@
 // lambda^c is a pair of floats, because its rounding would grow with the number of chunks.
 //
 // Warps: 0-3 turn S into P, rescale O and write the outputs (a thread is a token); 4-11 make
-// K'^T in tensor memory (a thread is a key channel) and carry the state (a thread is a key
-// channel and half of the value columns); 12 moves tiles by TMA; 13 issues the products.
+// K'^T in tensor memory, the two groups of four by turns (ldmatrix transposes the K tile);
+// 12-19 carry the state (a thread is a key channel and half of the value columns); 20 moves
+// tiles by TMA; 21 issues the products.  Their order, half of U, Q K^T, Q S0, the other half of
+// U, P V, gives every hand-over between warps the time of another product.
 // Shared memory holds two stages of q, k, v (192 KB) and the state as an operand (32 KB); the
 // outputs of a chunk leave through its q tile.  Tiles are two boxes of 64 channels x 128
 // tokens in the 128-byte swizzle, which serves as K-major operand (channels contracted) and
@@ -36,8 +38,11 @@ namespace {
 using namespace tcx;
 
 constexpr int kC = 128, kD = 128;
-constexpr int kRowWarps = 4, kStateWarps = 8, kThreads = 32 * (kRowWarps + kStateWarps + 2);
-constexpr int kTmaWarp = kRowWarps + kStateWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kRowWarps = 4, kKeyWarps = 8, kStateWarps = 8;
+constexpr int kStateWarp0 = kRowWarps + kKeyWarps, kTmaWarp = kStateWarp0 + kStateWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kLaunchRegs = 80, kKeyRegs = 64, kStateRegs = 96;
+static_assert(kKeyWarps * (kLaunchRegs - kKeyRegs) >= kStateWarps * (kStateRegs - kLaunchRegs), "registers moved");
 
 // shared memory
 constexpr uint32_t kHalf = 64 * kC * 2, kTile = 2 * kHalf;        // 16 KB box, 32 KB tile
@@ -47,16 +52,18 @@ constexpr uint32_t SM_WK = SM_WP + 256 * 4;           // [2][128] f_write lambda
 constexpr uint32_t SM_PW = SM_WK + 2 * 128 * 4;       // [129] lambda^n
 constexpr uint32_t SM_BAR = SM_PW + 132 * 4;
 enum Bar {
-    FULL_Q = 0, FULL_K = 2, FULL_V = 4, FREE_K = 6, FREE_V = 8, OUT_READY = 10, KP_READY = 12, KP_FREE = 14,
-    S_READY = 16, QS_READY, PV_GO, PV_DONE, O_FREE, U_READY, U_FREE, S0_READY, kBars
+    FULL_Q = 0, FULL_K = 2, FULL_V = 4, FREE_K = 6, FREE_V = 8, OUT_READY = 10, KP_READY = 12, KP_FREE = 17,
+    S_READY = 22, QS_READY, PV_GO, PV_DONE, O_FREE, U_READY, U_FREE, S0_READY, kBars
 };
 constexpr uint32_t SM_TMEM = SM_BAR + 8 * kBars;
 constexpr uint32_t SM_TOTAL = SM_TMEM + 16;
 static_assert(SM_TOTAL <= 227 * 1024, "shared memory of a CTA");
 
 // tensor memory columns
-constexpr uint32_t TM_S = 0, TM_O = 128, TM_U = 256, TM_KP = 384;   // TM_KP: two slots of 32 tokens x 3 parts
-constexpr uint32_t kKpSlot = 48, kKpPart = 16;
+constexpr uint32_t TM_S = 0, TM_P = 0, TM_O = 128, TM_U = 256, TM_KP = 384;
+constexpr uint32_t kKpPart = 8, kKpSlot = 3 * kKpPart;         // a slot: 16 tokens x 3 parts
+constexpr int kKpSlots = 5;
+static_assert(TM_KP + kKpSlots * kKpSlot <= 512 && KP_FREE == KP_READY + kKpSlots && S_READY == KP_FREE + kKpSlots, "slots");
 
 struct LaMaps {
     CUtensorMap q[kLaMaxPasses], k[kLaMaxPasses], v[kLaMaxPasses], out[kLaMaxPasses];
@@ -97,15 +104,45 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&x);
 }
 
-// fp32 as the sum of three bf16: the 24 bits cut into 8 + 8 + 8.
-__device__ __forceinline__ void cut3(float x, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+__device__ __forceinline__ bool elect_one()
 {
-    hi = __float_as_uint(x) & 0xffff0000u;
-    const float r = x - __uint_as_float(hi);
-    mid = __float_as_uint(r) & 0xffff0000u;
-    lo = __float_as_uint(r - __uint_as_float(mid));
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
-__device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+
+// Registers move from the key warps to the state warps, within what the block was launched with.
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+
+// Four 8 x 8 matrices of 16-bit elements, transposed: thread t gets rows 2 (t % 4) and + 1 of
+// column t / 4 of each.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t saddr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+}
+// Sixteen lanes x eight columns: thread t's registers are (lane t / 4, column t % 4), (lane
+// t / 4 + 8, same column), then the same four columns on.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};"
+                 :: "r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Two products k w (k a packed pair of bf16) as sums of three bf16 each: the 24 bits of the
+// fp32 product cut into 8 + 8 + 8.
+__device__ __forceinline__ void cut3(uint32_t k, float2 w, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
+    const float2 x = mul2(make_float2(__uint_as_float(k << 16), __uint_as_float(k & 0xffff0000u)), w);
+    const uint32_t x0 = __float_as_uint(x.x), x1 = __float_as_uint(x.y);
+    hi = __byte_perm(x0, x1, 0x7632);
+    const float2 r = sub2(x, make_float2(__uint_as_float(x0 & 0xffff0000u), __uint_as_float(x1 & 0xffff0000u)));
+    const uint32_t r0 = __float_as_uint(r.x), r1 = __float_as_uint(r.y);
+    mid = __byte_perm(r0, r1, 0x7632);
+    const float2 q = sub2(r, make_float2(__uint_as_float(r0 & 0xffff0000u), __uint_as_float(r1 & 0xffff0000u)));
+    lo = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632);
+}
 
 // STATES_ONLY: the segment's own state from zero goes to slot seg + 1 of the workspace; no
 // outputs (warps 0-3 idle, no q).
@@ -136,9 +173,10 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     float *sPW = reinterpret_cast<float *>(smem + SM_PW);
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const int count = (i >= FREE_K && i < FREE_V) ? (STATES_ONLY ? kStateWarps : kStateWarps + 1)
+            const int count = (i >= FREE_K && i < FREE_V) ? (STATES_ONLY ? kKeyWarps : kKeyWarps + 1)
                               : (i >= OUT_READY && i < KP_READY) || i == PV_GO || i == O_FREE ? kRowWarps
-                              : (i >= KP_READY && i < KP_FREE) || i == U_FREE || i == S0_READY ? kStateWarps : 1;
+                              : (i >= KP_READY && i < KP_FREE) ? kKeyWarps / 2
+                              : i == U_FREE || i == S0_READY ? kStateWarps : 1;
             mbar_init(bar(i), (uint32_t)count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -164,8 +202,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         sWK[tid] = ps.f_write * sPW[rev ? j + 1 : max(c - 1 - j, 0)];
     }
     __syncthreads();
-    uint32_t tm;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tm) : "r"(sb + SM_TMEM));
+    constexpr uint32_t tm = 0;              // all 512 columns: they begin at 0
 
     bool ok = true;                         // false: a wait of this role ran out
     auto wait = [&](int i, uint32_t parity) {           // by one thread
@@ -189,7 +226,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
             const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
             for (int it = 0; it < nchunks; ++it) {
                 const int c = tokens_of(chunk_at(it)), st = it & 1;
-                // ---- P from S, in place
+                // ---- P from S
                 if (!wait_warp(S_READY, it)) break;
                 tc_fence_after();
 #pragma unroll
@@ -205,7 +242,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
 #pragma unroll
                         for (int j = 0; j < 16; ++j) p[j] = 0u;
                     }
-                    tmem_st16u(row + TM_S + 16 * cb, p);
+                    tmem_st16u(row + TM_P + 16 * cb, p);
                 }
                 // ---- O <- f_inter lambda^(.) O
                 if (!wait_warp(QS_READY, it)) break;
@@ -246,11 +283,59 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 }
             }
         }
+    } else if (warp < kStateWarp0) {
+        // ---- K'^T: slots of 16 tokens, this group's every second one; 32 key channels a warp
+        const int quad = warp & 3, group = (warp - kRowWarps) >> 2;
+        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_KP;
+        int slot = group, use = 0;                              // of the ring: every second one
+        reg_dec<kKeyRegs>();
+        // ldmatrix: lanes 8 m .. 8 m + 7 name the rows (tokens) of matrix m: tokens 8 (m / 2) ..,
+        // channels 8 (m % 2) .. of the 16 of a half-warp; 16-byte pieces swizzled by token % 8
+        const int jr = lane & 7, m = lane >> 3, piece = 4 * (quad & 1) + (m & 1);
+        const uint32_t kt = sb + SM_K + (quad >> 1) * kHalf + (uint32_t)((16 * group + 8 * (m >> 1) + jr) * 128);
+        const uint32_t off0 = (uint32_t)((piece ^ jr) << 4), off1 = (uint32_t)(((piece + 2) ^ jr) << 4);
+        for (int it = 0; it < nchunks; ++it) {
+            const int st = it & 1;
+            const float *wk = sWK + (tokens_of(chunk_at(it)) != kC ? kC : 0) + 16 * group + 2 * (lane & 3);
+            if (!wait_warp(FULL_K + st, it >> 1)) break;
+#pragma unroll 1
+            for (int s4 = 0; s4 < 4; ++s4) {
+                const float2 w0 = *reinterpret_cast<const float2 *>(wk + 32 * s4);
+                const float2 w1 = *reinterpret_cast<const float2 *>(wk + 32 * s4 + 8);
+                const uint32_t src = kt + st * kTile + s4 * (32 * 128);
+                uint32_t k0[4], k1[4], hi[8], mid[8], lo[8];
+                ldmatrix4_trans(src + off0, k0);
+                ldmatrix4_trans(src + off1, k1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    cut3(k0[e], e < 2 ? w0 : w1, hi[e], mid[e], lo[e]);
+                    cut3(k1[e], e < 2 ? w0 : w1, hi[4 + e], mid[4 + e], lo[4 + e]);
+                }
+                if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const uint32_t dst = row + ((uint32_t)(4 * e) << 16) + slot * kKpSlot;
+                    tmem_st_16x8(dst, hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
+                    tmem_st_16x8(dst + kKpPart, mid[e], mid[e + 1], mid[e + 2], mid[e + 3]);
+                    tmem_st_16x8(dst + 2 * kKpPart, lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(KP_READY + slot);
+                slot += 2;
+                if (slot >= kKpSlots) { slot -= kKpSlots; ++use; }
+            }
+            if (!ok) break;
+            arrive_warp(FREE_K + st);
+        }
     } else if (warp < kTmaWarp) {
-        const int ws = warp - kRowWarps, quad = warp & 3, part = ws >> 2;
-        const int r = 32 * quad + lane;                         // key channel
-        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16);
-        float S[64];                                            // value columns 64 part ..
+        // ---- the state: key channel r, value columns 64 part ..
+        const int quad = warp & 3, part = (warp - kStateWarp0) >> 2;
+        const int r = 32 * quad + lane;
+        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_U + 64 * part;
+        reg_inc<kStateRegs>();
+        float S[64];
         {
             const float *s0 = STATES_ONLY ? nullptr : slots ? slots + (size_t)seg * kD * kD
                               : ps.s0 ? ps.s0 + (size_t)bh * kD * kD : nullptr;
@@ -278,64 +363,30 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         };
         if (!STATES_ONLY) publish();
         const double whole = la_power(a.log_decay, h, kC), ragged = la_power(a.log_decay, h, c_last);
+        const float2 l_whole = make_float2((float)whole, (float)(whole - (double)(float)whole));
+        const float2 l_ragged = make_float2((float)ragged, (float)(ragged - (double)(float)ragged));
         for (int it = 0; it < nchunks; ++it) {
-            const int n = chunk_at(it), st = it & 1;
-            const bool tail = tokens_of(n) != kC;
-            if (!wait_warp(FULL_K + st, it >> 1)) break;
-            // ---- K'^T: this warp's 16 tokens of each quarter, pairs of tokens packed
-            const uint8_t *kt = smem + SM_K + st * kTile + (quad >> 1) * kHalf;
-            const float *wk = sWK + (tail ? kC : 0);
-#pragma unroll 1
-            for (int qt = 0; qt < 4; ++qt) {
-                const int slot = qt & 1, use = 2 * it + (qt >> 1), j0 = 32 * qt + 16 * part;
-                if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) break;
-                tc_fence_after();
-                uint32_t hi[8], mid[8], lo[8];
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 w = *reinterpret_cast<const float4 *>(wk + j0 + j);
-                    const float wj[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t x[3][4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // row j of the tile: 16-byte pieces swizzled by j & 7
-                        const int jj = j0 + j + e, col = 2 * (r & 63);
-                        const uint16_t u = *reinterpret_cast<const uint16_t *>(kt + jj * 128 + (col ^ ((jj & 7) << 4)));
-                        cut3(__uint_as_float((uint32_t)u << 16) * wj[e], x[0][e], x[1][e], x[2][e]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        hi[j / 2 + e] = upper_halves(x[0][2 * e], x[0][2 * e + 1]);
-                        mid[j / 2 + e] = upper_halves(x[1][2 * e], x[1][2 * e + 1]);
-                        lo[j / 2 + e] = upper_halves(x[2][2 * e], x[2][2 * e + 1]);
-                    }
-                }
-                const uint32_t kp = row + TM_KP + slot * kKpSlot + 8 * part;
-                tmem_st8u(kp, hi);
-                tmem_st8u(kp + kKpPart, mid);
-                tmem_st8u(kp + 2 * kKpPart, lo);
-                tmem_wait_st();
-                tc_fence_before();
-                arrive_warp(KP_READY + slot);
-            }
-            if (!ok) break;
-            arrive_warp(FREE_K + st);
-            // ---- S <- lambda^c S + U
+            // S <- lambda^c S + U
             if (!wait_warp(U_READY, it)) break;
             tc_fence_after();
-            const double lc = tail ? ragged : whole;
-            const float lh = (float)lc, ll = (float)(lc - (double)lh);
+            const float2 l = tokens_of(chunk_at(it)) != kC ? l_ragged : l_whole;
+            const float2 lh = make_float2(l.x, l.x), ll = make_float2(l.y, l.y);
 #pragma unroll
-            for (int x = 0; x < 64; x += 32) {
-                float u[32];
-                tmem_ld32(row + TM_U + 64 * part + x, u);
+            for (int x = 0; x < 64; x += 16) {
+                float u[16];
+                tmem_ld16(row + x, u);
 #pragma unroll
-                for (int y = 0; y < 32; ++y) S[x + y] = fmaf(lh, S[x + y], fmaf(ll, S[x + y], u[y]));
+                for (int y = 0; y < 16; y += 2) {
+                    const float2 s = make_float2(S[x + y], S[x + y + 1]);
+                    const float2 n = fma2(lh, s, fma2(ll, s, make_float2(u[y], u[y + 1])));
+                    S[x + y] = n.x;
+                    S[x + y + 1] = n.y;
+                }
             }
             tc_fence_before();
             arrive_warp(U_FREE);
             if (!STATES_ONLY && it + 1 < nchunks) {
-                if (!wait_warp(QS_READY, it)) break;                 // the operand of this chunk has been read
+                if (!wait_warp(QS_READY, it)) break;            // the operand of this chunk has been read
                 publish();
             }
         }
@@ -388,67 +439,75 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     if (!STATES_ONLY) mbar_wait(bar(FULL_Q + (it & 1)), (it >> 1) & 1);
                 }
         }
-    } else if (lane == 0) {
+    } else {
+        // The whole warp walks the loop and one elected lane issues, so that descriptors stay in
+        // uniform registers: under `lane == 0` each product took 100 cycles to issue, against
+        // the 64 it runs.
         constexpr uint32_t id_nt = idesc_bf16(128, 128, 0, 0), id_nn = idesc_bf16(128, 128, 0, 1);
-        for (int it = 0; it < nchunks; ++it) {
-            const int st = it & 1;
-            const uint32_t q = sb + SM_Q + st * kTile, k = sb + SM_K + st * kTile, v = sb + SM_V + st * kTile;
-            if (!STATES_ONLY) {
-                // S = Q K^T: a K step of 16 channels is 32 bytes inside the swizzled rows
-                if (!wait(FULL_Q + st, it >> 1) || !wait(FULL_K + st, it >> 1)) break;
-                if (it > 0 && !wait(PV_DONE, it - 1)) break;
-                tc_fence_after();
+        const uint64_t dq = desc_sw128(sb + SM_Q, 16), dk = desc_sw128(sb + SM_K, 16), dv = desc_sw128(sb + SM_V, kHalf);
+        const uint64_t ds = desc_sw128(sb + SM_S0, kHalf);
+        // A K step of 16 channels is 32 bytes inside the swizzled rows of a K-major tile, 16 rows
+        // of an MN-major one (addresses in 16 bytes).
+        auto k_major = [](int ks) { return (uint64_t)((ks >> 2) * (kHalf >> 4) + (ks & 3) * 2); };
+        int slot = 0, use = 0;
+        // U (+)= K'^T V over 64 tokens: a K step of three parts per slot
+        auto update = [&](uint64_t v, int half) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-                    umma_bf16(tm + TM_S, desc_sw128(q + off, 16), desc_sw128(k + off, 16), id_nt, ks > 0);
-                }
-                umma_commit(bar(S_READY));
-                umma_commit(bar(FREE_K + st));
-            }
-            if (it > 0 && !wait(U_FREE, it - 1)) break;
-            if (!wait(FULL_V + st, it >> 1)) break;
-#pragma unroll 1
-            for (int qt = 0; qt < 4; ++qt) {
-                // U += K'^T V over 32 tokens: two K steps of three parts
-                const int slot = qt & 1;
-                if (!wait(KP_READY + slot, 2 * it + (qt >> 1))) break;
+            for (int ks = 4 * half; ks < 4 * half + 4; ++ks) {
+                if (!wait_warp(KP_READY + slot, use)) return false;
                 tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const uint64_t dv = desc_sw128(v + (2 * qt + ks) * 2048, kHalf);
+                if (elect_one()) {
 #pragma unroll
                     for (int p = 0; p < 3; ++p)
-                        umma_bf16_ta(tm + TM_U, tm + TM_KP + slot * kKpSlot + p * kKpPart + 8 * ks, dv, id_nn,
-                                     qt > 0 || ks > 0 || p > 0);
+                        umma_bf16_ta(tm + TM_U, tm + TM_KP + slot * kKpSlot + p * kKpPart, v + (uint64_t)(ks * 128), id_nn,
+                                     ks > 0 || p > 0);
+                    umma_commit(bar(KP_FREE + slot));
+                    if (ks == 7) umma_commit(bar(U_READY));
                 }
-                umma_commit(bar(KP_FREE + slot));
-                if (qt == 3) {
-                    umma_commit(bar(U_READY));
-                    if (STATES_ONLY) umma_commit(bar(FREE_V + st));
-                }
-                if (!STATES_ONLY && qt == 1) {
-                    // O = Q S0
-                    if (!wait(S0_READY, it) || (it > 0 && !wait(O_FREE, it - 1))) break;
-                    tc_fence_after();
+                if (++slot == kKpSlots) { slot = 0; ++use; }
+            }
+            return true;
+        };
+        for (int it = 0; it < nchunks; ++it) {
+            const int st = it & 1;
+            const uint64_t q = dq + (uint64_t)(st * (kTile >> 4)), k = dk + (uint64_t)(st * (kTile >> 4));
+            const uint64_t v = dv + (uint64_t)(st * (kTile >> 4));
+            if (!wait_warp(FULL_V + st, it >> 1)) break;
+            if (it > 0 && !wait_warp(U_FREE, it - 1)) break;
+            if (!update(v, 0)) break;
+            if (!STATES_ONLY) {
+                // S = Q K^T
+                if (!wait_warp(FULL_Q + st, it >> 1) || !wait_warp(FULL_K + st, it >> 1)) break;
+                if (it > 0 && !wait_warp(PV_DONE, it - 1)) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16(tm + TM_O, desc_sw128(q + (ks >> 2) * kHalf + (ks & 3) * 32, 16),
-                                  desc_sw128(sb + SM_S0 + ks * 2048, kHalf), id_nn, ks > 0);
+                    for (int ks = 0; ks < 8; ++ks) umma_bf16(tm + TM_S, q + k_major(ks), k + k_major(ks), id_nt, ks > 0);
+                    umma_commit(bar(S_READY));
+                    umma_commit(bar(FREE_K + st));
+                }
+                // O = Q S0
+                if (!wait_warp(S0_READY, it) || (it > 0 && !wait_warp(O_FREE, it - 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) umma_bf16(tm + TM_O, q + k_major(ks), ds + (uint64_t)(ks * 128), id_nn, ks > 0);
                     umma_commit(bar(QS_READY));
                 }
             }
-            if (!ok) break;
+            if (!update(v, 1)) break;
             if (!STATES_ONLY) {
                 // O += P V
-                if (!wait(PV_GO, it)) break;
+                if (!wait_warp(PV_GO, it)) break;
                 tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    umma_bf16_ta(tm + TM_O, tm + TM_S + 8 * ks, desc_sw128(v + ks * 2048, kHalf), id_nn, 1);
-                umma_commit(bar(PV_DONE));
-                umma_commit(bar(FREE_V + st));
-            }
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16_ta(tm + TM_O, tm + TM_P + 8 * ks, v + (uint64_t)(ks * 128), id_nn, 1);
+                    umma_commit(bar(PV_DONE));
+                    umma_commit(bar(FREE_V + st));
+                }
+            } else if (elect_one()) umma_commit(bar(FREE_V + st));
         }
     }
     __syncwarp();
@@ -513,6 +572,10 @@ cudaError_t launch_la_tc(const LaArgs &a, bool states_only, cudaStream_t stream)
     auto kernel = states_only ? la_tc_kernel<true> : la_tc_kernel<false>;
     if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM_TOTAL)) != cudaSuccess)
         return e;
+    // the move of registers between warps is sized for this many: with fewer it would wait for ever
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
     const size_t grid = (size_t)a.npass * a.B * a.H * (states_only ? a.nseg - 1 : a.nseg);
     kernel<<<(unsigned)grid, kThreads, SM_TOTAL, stream>>>(a, maps);
     e = cudaGetLastError();
