@@ -18,7 +18,6 @@ library is not built, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -156,11 +155,18 @@ def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _device(device: torch.device):
-    """Makes the tensors' device the current one for a launch, where it is not."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _need_all(index: int, dtype, tensors):
+    """:func:`_need` for calls whose own time is a few microseconds: (tensor or None, name,
+    shape, dtype or None for ``dtype``), all on CUDA device ``index``.  What is wrong is said
+    by :func:`_need`."""
+    for t, name, shape, dt in tensors:
+        if t is not None and not (t.shape == shape and t.dtype is (dt or dtype) and t.is_contiguous()
+                                  and t.get_device() == index):
+            _need(t, name, shape, dt or dtype, torch.device("cuda", index))
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -585,15 +591,30 @@ def gdn_decode_step(q, k, v, log_alpha, beta, state, *, out=None, scale: float =
     return _decode("kda_gdn_decode_step", shape, q, k, v, log_alpha, beta, state, out, scale)
 
 
+def _launch(index: int, fn, *args) -> int:
+    """fn(*args, current stream) with the tensors' device as the current one."""
+    if index == torch.cuda.current_device():
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index))
+
+
+def _address(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _la_workspace(fn, q, dk, dv, code, workspace, where):
-    """The workspace of a linear-attention call and its bytes: the caller's, or a new one
-    where the sizes need any (taken from torch's allocator on the current stream)."""
+    """Address and bytes of a linear-attention call's workspace, and the tensor: the caller's,
+    or a new one where the sizes need any (from torch's allocator, on the current stream)."""
     B, T, H = q.shape[:3]
-    if workspace is not None:
-        _need_workspace(workspace, q.device, where)
-        return workspace, workspace.numel() * workspace.element_size()
-    n = fn(B, T, H, dk, dv, code)
-    return (torch.empty(n, dtype=torch.uint8, device=q.device) if n else None), n
+    if workspace is None:
+        n = fn(B, T, H, dk, dv, code)
+        if not n:
+            return None, 0, None
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        return workspace.data_ptr(), n, workspace
+    _need_workspace(workspace, q.device, where)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, backward=False) -> int:
@@ -603,16 +624,16 @@ def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, backward=False) ->
     return int(fn(int(B), int(T), int(H), int(dk), int(dv), KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
 
 
-def _need_la(q, k, v, log_decay, where):
-    """What the linear-attention calls check of their inputs; q's shape tells B, T and H."""
-    lead, dk, dev = tuple(q.shape[:-1]), q.shape[-1], q.device
-    _on_cuda(dev, where)
+def _need_la(q, k, v, log_decay, where, *more):
+    """What the linear-attention calls check of their inputs; q's shape tells B, T and H.
+    ``more``: further rows of :func:`_need_all`."""
+    if q.device.type != "cuda":
+        _on_cuda(q.device, where)
     code = _dtype_code(q)
-    _need(q, "q", lead + (dk,), q.dtype, dev)
-    _need(k, "k", lead + (dk,), q.dtype, dev)
-    _need(v, "v", lead + (v.shape[-1],), q.dtype, dev)
-    if log_decay is not None:
-        _need(log_decay, "log_decay", (q.shape[-2],), torch.float32, dev)
+    lead = q.shape[:-1]
+    _need_all(q.get_device(), q.dtype, ((q, "q", q.shape, None), (k, "k", q.shape, None),
+                                        (v, "v", lead + v.shape[-1:], None),
+                                        (log_decay, "log_decay", q.shape[-2:-1], torch.float32)) + more)
     return code
 
 
@@ -629,25 +650,20 @@ def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=
     :func:`la_workspace_bytes` bytes (allocated when None and needed).
     """
     lib = load()
-    code = _need_la(q, k, v, log_decay, "kda_la_forward")
     B, T, H, dk = q.shape
-    dv, dev = v.shape[-1], q.device
-    if initial_state is not None:
-        _need(initial_state, "initial_state", (B, H, dk, dv), torch.float32, dev)
+    dv = v.shape[-1]
+    state = (B, H, dk, dv)
+    code = _need_la(q, k, v, log_decay, "kda_la_forward", (initial_state, "initial_state", state, torch.float32),
+                    (out, "out", (B, T, H, dv), None), (final_state, "final_state", state, torch.float32))
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
-    else:
-        _need(out, "out", (B, T, H, dv), q.dtype, dev)
-    if final_state is not None:
-        _need(final_state, "final_state", (B, H, dk, dv), torch.float32, dev)
-    elif return_final_state:
-        final_state = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-    ws, nbytes = _la_workspace(lib.kda_la_forward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_forward")
-    with _device(dev):
-        st = lib.kda_la_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(out),
-                                _ptr(final_state), B, T, H, dk, dv, code, float(scale), _ptr(ws), nbytes,
-                                _stream(dev))
-    _check(st, "kda_la_forward")
+        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+    if final_state is None and return_final_state:
+        final_state = torch.empty(state, dtype=torch.float32, device=q.device)
+    ws, nbytes, _hold = _la_workspace(lib.kda_la_forward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_forward")
+    st = _launch(q.get_device(), lib.kda_la_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
+                 _address(initial_state), out.data_ptr(), _address(final_state), B, T, H, dk, dv, code, scale, ws, nbytes)
+    if st:
+        _check(st, "kda_la_forward")
     return out, final_state
 
 
@@ -661,25 +677,21 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
     ``initial_state_grad``).  ``log_decay`` is a constant: it has no gradient.
     """
     lib = load()
-    code = _need_la(q, k, v, log_decay, "kda_la_backward")
     B, T, H, dk = q.shape
-    dv, dev = v.shape[-1], q.device
-    _need(grad_out, "grad_out", (B, T, H, dv), q.dtype, dev)
-    if initial_state is not None:
-        _need(initial_state, "initial_state", (B, H, dk, dv), torch.float32, dev)
-    if grad_final_state is not None:
-        _need(grad_final_state, "grad_final_state", (B, H, dk, dv), torch.float32, dev)
-    g = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-             dinitial_state=torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-             if initial_state_grad else None)
-    ws, nbytes = _la_workspace(lib.kda_la_backward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_backward")
-    with _device(dev):
-        st = lib.kda_la_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(initial_state), _ptr(grad_out),
-                                 _ptr(grad_final_state), _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]),
-                                 _ptr(g["dinitial_state"]), B, T, H, dk, dv, code, float(scale), _ptr(ws), nbytes,
-                                 _stream(dev))
-    _check(st, "kda_la_backward")
-    return g
+    dv = v.shape[-1]
+    state = (B, H, dk, dv)
+    code = _need_la(q, k, v, log_decay, "kda_la_backward", (grad_out, "grad_out", (B, T, H, dv), None),
+                    (initial_state, "initial_state", state, torch.float32),
+                    (grad_final_state, "grad_final_state", state, torch.float32))
+    dq, dkey, dval = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ds0 = torch.empty(state, dtype=torch.float32, device=q.device) if initial_state_grad else None
+    ws, nbytes, _hold = _la_workspace(lib.kda_la_backward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_backward")
+    st = _launch(q.get_device(), lib.kda_la_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
+                 _address(initial_state), grad_out.data_ptr(), _address(grad_final_state), dq.data_ptr(),
+                 dkey.data_ptr(), dval.data_ptr(), _address(ds0), B, T, H, dk, dv, code, scale, ws, nbytes)
+    if st:
+        _check(st, "kda_la_backward")
+    return dict(dq=dq, dk=dkey, dv=dval, dinitial_state=ds0)
 
 
 class LAFunction(torch.autograd.Function):
@@ -712,18 +724,16 @@ def la_decode_step(q, k, v, log_decay, state, *, out=None, scale: float = 0.0):
     ``[B,H,dk,dv]`` fp32.  Returns ``out [B,H,dv]`` in the dtype of q.
     """
     lib = load()
-    code = _need_la(q, k, v, log_decay, "kda_la_decode_step")
     B, H, dk = q.shape
-    dv, dev = v.shape[-1], q.device
-    _need(state, "state", (B, H, dk, dv), torch.float32, dev)
+    dv = v.shape[-1]
+    code = _need_la(q, k, v, log_decay, "kda_la_decode_step", (state, "state", (B, H, dk, dv), torch.float32),
+                    (out, "out", (B, H, dv), None))
     if out is None:
-        out = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
-    else:
-        _need(out, "out", (B, H, dv), q.dtype, dev)
-    with _device(dev):
-        st = lib.kda_la_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(out), B, H, dk, dv,
-                                    code, float(scale), _stream(dev))
-    _check(st, "kda_la_decode_step")
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+    st = _launch(q.get_device(), lib.kda_la_decode_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
+                 state.data_ptr(), out.data_ptr(), B, H, dk, dv, code, scale)
+    if st:
+        _check(st, "kda_la_decode_step")
     return out
 
 
@@ -749,33 +759,30 @@ def paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths, *, out=No
     B, H, D = q.shape
     num_pages, page_size, Hkv = k_cache.shape[:3]
     max_pages = block_table.shape[-1]
-    dev = q.device
-    _on_cuda(dev, "kda_paged_decode_step")
-    code = _dtype_code(q)
-    _need(q, "q", (B, H, D), q.dtype, dev)
+    if q.device.type != "cuda":
+        _on_cuda(q.device, "kda_paged_decode_step")
     if (k is None) != (v is None):
         raise ValueError("kda_paged_decode_step: k and v are given together or not at all")
-    if k is not None:
-        _need(k, "k", (B, Hkv, D), q.dtype, dev)
-        _need(v, "v", (B, Hkv, D), q.dtype, dev)
-    _need(k_cache, "k_cache", (num_pages, page_size, Hkv, D), q.dtype, dev)
-    _need(v_cache, "v_cache", (num_pages, page_size, Hkv, D), q.dtype, dev)
-    _need(block_table, "block_table", (B, max_pages), torch.int32, dev)
-    _need(lengths, "lengths", (B,), torch.int32, dev)
+    code = _dtype_code(q)
+    cache = (num_pages, page_size, Hkv, D)
+    _need_all(q.get_device(), q.dtype,
+              ((q, "q", q.shape, None), (k, "k", (B, Hkv, D), None), (v, "v", (B, Hkv, D), None),
+               (k_cache, "k_cache", cache, None), (v_cache, "v_cache", cache, None),
+               (block_table, "block_table", (B, max_pages), torch.int32), (lengths, "lengths", (B,), torch.int32),
+               (out, "out", (B, H, D), None)))
     if out is None:
-        out = torch.empty((B, H, D), dtype=q.dtype, device=dev)
-    else:
-        _need(out, "out", (B, H, D), q.dtype, dev)
+        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
     if workspace is None:
-        workspace = torch.empty(lib.kda_paged_decode_workspace_bytes(H, Hkv, D, code), dtype=torch.uint8, device=dev)
+        nbytes = lib.kda_paged_decode_workspace_bytes(H, Hkv, D, code)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     else:
-        _need_workspace(workspace, dev, "kda_paged_decode_step")
-    with _device(dev):
-        st = lib.kda_paged_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                       _ptr(lengths), _ptr(out), B, H, Hkv, D, num_pages, page_size, max_pages, code,
-                                       float(scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       _stream(dev))
-    _check(st, "kda_paged_decode_step")
+        _need_workspace(workspace, q.device, "kda_paged_decode_step")
+        nbytes = workspace.numel() * workspace.element_size()
+    st = _launch(q.get_device(), lib.kda_paged_decode_step, q.data_ptr(), _address(k), _address(v), k_cache.data_ptr(),
+                 v_cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), B, H, Hkv, D, num_pages,
+                 page_size, max_pages, code, scale, workspace.data_ptr(), nbytes)
+    if st:
+        _check(st, "kda_paged_decode_step")
     return out
 
 

@@ -3,6 +3,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <stdint.h>
 
 #include "kda.h"
@@ -107,6 +108,25 @@ cudaError_t take_device_status(unsigned int *status);
 
 // Counts one kernel enqueued through the library (see kda_launch_count).
 void note_launch();
+
+// Sets a kernel's dynamic shared memory on the current device, the first time it is launched
+// there.  `done` is the call site's own: one flag per device, so that a later launch asks the
+// runtime for the device alone.
+struct OncePerDevice {
+    std::atomic<bool> done[64];
+};
+template <typename Kernel>
+cudaError_t set_shared_memory(Kernel kernel, int bytes, OncePerDevice &once)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && once.done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && known) once.done[dev].store(true, std::memory_order_release);
+    return e;
+}
 
 // kda_last_cuda_error of this thread: cleared at the start of a call, set by the first
 // failure (returns KDA_ERR_CUDA).

@@ -223,7 +223,8 @@ cudaError_t launch_typed(const LaArgs &a, cudaStream_t stream)
 {
     auto kernel = la_simt_kernel<DK, DV, InT, STATES_ONLY>;
     constexpr size_t bytes = LaSmem<DK, DV>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    static OncePerDevice once;
+    cudaError_t e = set_shared_memory(kernel, (int)bytes, once);
     if (e != cudaSuccess) return e;
     const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
     kernel<<<(unsigned)((size_t)a.npass * a.B * a.H * nwork), kThreads, bytes, stream>>>(a);

@@ -12,12 +12,18 @@
 // written as three bf16 parts that hold all 24 bits of the fp32 product, U starts afresh
 // every chunk (the tensor core's accumulation is short) and is added in registers, and
 // lambda^c is a pair of floats, because its rounding would grow with the number of chunks.
+// The third part is left out where it cannot be seen: two parts are off by at most 2^-17 of a
+// term, so they do for a state that only enters bf16 products, and for terms that fade to
+// less than 2^-6 of their size before the state is written out (their errors to 2^-23).  The
+// kernel runs into the power limit (1.5 of 1.97 GHz at B4 H32 T16384, 980 W), and U is half
+// of its products.
 //
 // Warps: 0-3 turn S into P, rescale O and write the outputs (a thread is a token); 4-11 make
 // K'^T in tensor memory, the two groups of four by turns (ldmatrix transposes the K tile);
 // 12-19 carry the state (a thread is a key channel and half of the value columns); 20 moves
-// tiles by TMA; 21 issues the products.  Their order, half of U, Q K^T, Q S0, the other half of
-// U, P V, gives every hand-over between warps the time of another product.
+// tiles by TMA; 21 issues Q K^T, Q S0 and P V, 22 the steps of U: a wait and an issue take a
+// warp about as long as the tensor core takes for a step, so one warp for all of them would
+// leave it idle half of the time (B4 H32 T16384: 452 us with one, LAT2 us with two).
 // Shared memory holds two stages of q, k, v (192 KB) and the state as an operand (32 KB); the
 // outputs of a chunk leave through its q tile.  Tiles are two boxes of 64 channels x 128
 // tokens in the 128-byte swizzle, which serves as K-major operand (channels contracted) and
@@ -39,9 +45,9 @@ using namespace tcx;
 
 constexpr int kC = 128, kD = 128;
 constexpr int kRowWarps = 4, kKeyWarps = 8, kStateWarps = 8;
-constexpr int kStateWarp0 = kRowWarps + kKeyWarps, kTmaWarp = kStateWarp0 + kStateWarps, kMmaWarp = kTmaWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kLaunchRegs = 80, kKeyRegs = 64, kStateRegs = 96;
+constexpr int kStateWarp0 = kRowWarps + kKeyWarps, kTmaWarp = kStateWarp0 + kStateWarps, kMmaWarp = kTmaWarp + 1, kUpdateWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kUpdateWarp + 1);
+constexpr int kLaunchRegs = 80, kKeyRegs = 56, kStateRegs = 104;
 static_assert(kKeyWarps * (kLaunchRegs - kKeyRegs) >= kStateWarps * (kStateRegs - kLaunchRegs), "registers moved");
 
 // shared memory
@@ -50,28 +56,52 @@ constexpr uint32_t SM_Q = 0, SM_K = SM_Q + 2 * kTile, SM_V = SM_K + 2 * kTile, S
 constexpr uint32_t SM_WP = SM_S0 + kTile;             // [256] f_intra lambda^(i-j) at i - j + 127, zeros beyond
 constexpr uint32_t SM_WK = SM_WP + 256 * 4;           // [2][128] f_write lambda^(.) of a whole and of the ragged chunk
 constexpr uint32_t SM_PW = SM_WK + 2 * 128 * 4;       // [129] lambda^n
-constexpr uint32_t SM_BAR = SM_PW + 132 * 4;
+constexpr uint32_t SM_LC = SM_PW + 132 * 4;           // [2] lambda^c of a whole and of the ragged chunk, two floats each
+constexpr uint32_t SM_BAR = SM_LC + 16;
+constexpr int kKpSlots = 5, kKpSlotsStates = 10;       // slots of K', of the two kernels
 enum Bar {
-    FULL_Q = 0, FULL_K = 2, FULL_V = 4, FREE_K = 6, FREE_V = 8, OUT_READY = 10, KP_READY = 12, KP_FREE = 17,
-    S_READY = 22, QS_READY, PV_GO, PV_DONE, O_FREE, U_READY, U_FREE, S0_READY, kBars
+    FULL_Q = 0, FULL_K = 2, FULL_V = 4, FREE_K = 6, FREE_V = 8, OUT_READY = 10, U_READY = 12, U_FREE = 14,
+    KP_READY = 16, KP_FREE = KP_READY + kKpSlotsStates, S_READY = KP_FREE + kKpSlotsStates, QS_READY, PV_GO, PV_DONE,
+    O_FREE, S0_READY, kBars
 };
 constexpr uint32_t SM_TMEM = SM_BAR + 8 * kBars;
 constexpr uint32_t SM_TOTAL = SM_TMEM + 16;
 static_assert(SM_TOTAL <= 227 * 1024, "shared memory of a CTA");
 
-// tensor memory columns
+// Tensor memory columns.  Without outputs, S and O make room for five more slots of K' and a
+// second U, so that a chunk's U is computed while the one before is added to the state.
 constexpr uint32_t TM_S = 0, TM_P = 0, TM_O = 128, TM_U = 256, TM_KP = 384;
 constexpr uint32_t kKpPart = 8, kKpSlot = 3 * kKpPart;         // a slot: 16 tokens x 3 parts
-constexpr int kKpSlots = 5;
-static_assert(TM_KP + kKpSlots * kKpSlot <= 512 && KP_FREE == KP_READY + kKpSlots && S_READY == KP_FREE + kKpSlots, "slots");
+static_assert(TM_KP + kKpSlots * kKpSlot <= 512 && (kKpSlotsStates - kKpSlots) * kKpSlot <= TM_O, "slots");
+__device__ __forceinline__ uint32_t kp_column(int slot)
+{
+    return slot < kKpSlots ? TM_KP + kKpSlot * (uint32_t)slot : TM_S + kKpSlot * (uint32_t)(slot - kKpSlots);
+}
 
 struct LaMaps {
     CUtensorMap q[kLaMaxPasses], k[kLaMaxPasses], v[kLaMaxPasses], out[kLaMaxPasses];
 };
 
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo)
+// Descriptors of 128-byte-swizzled tiles whose 8-row groups are 1024 bytes apart, in two
+// words: the lower one holds the address (in 16 bytes, so that steps are added to it) and the
+// leading stride, the upper one is the same for all of them.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool acc)
 {
-    return smem_desc(saddr, lbo, 1024u) | ((uint64_t)2 << 61);
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}\n"
+                 :: "r"(d), "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+// A in tensor memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "mov.b64 b, {%2, %3};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n"
+                 :: "r"(d), "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint32_t mbar, int c0, int c1, int c2, int c3)
@@ -98,6 +128,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(saddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
@@ -130,11 +175,14 @@ __device__ __forceinline__ void tmem_st_16x8(uint32_t taddr, uint32_t a, uint32_
                  :: "r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Two products k w (k a packed pair of bf16) as sums of three bf16 each: the 24 bits of the
-// fp32 product cut into 8 + 8 + 8.
-__device__ __forceinline__ void cut3(uint32_t k, float2 w, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+// Two products k w (k a packed pair of bf16) in fp32.
+__device__ __forceinline__ float2 scale_pair(uint32_t k, float2 w)
 {
-    const float2 x = mul2(make_float2(__uint_as_float(k << 16), __uint_as_float(k & 0xffff0000u)), w);
+    return mul2(make_float2(__uint_as_float(k << 16), __uint_as_float(k & 0xffff0000u)), w);
+}
+// x as the sum of three bf16: its 24 bits cut into 8 + 8 + 8.
+__device__ __forceinline__ void cut3(float2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo)
+{
     const uint32_t x0 = __float_as_uint(x.x), x1 = __float_as_uint(x.y);
     hi = __byte_perm(x0, x1, 0x7632);
     const float2 r = sub2(x, make_float2(__uint_as_float(x0 & 0xffff0000u), __uint_as_float(x1 & 0xffff0000u)));
@@ -142,6 +190,18 @@ __device__ __forceinline__ void cut3(uint32_t k, float2 w, uint32_t &hi, uint32_
     mid = __byte_perm(r0, r1, 0x7632);
     const float2 q = sub2(r, make_float2(__uint_as_float(r0 & 0xffff0000u), __uint_as_float(r1 & 0xffff0000u)));
     lo = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632);
+}
+
+// What a CTA works on.
+struct Item { int seg, bh, ip; };
+__device__ __forceinline__ Item item_at(const LaArgs &a, bool states_only, unsigned int id)
+{
+    const unsigned int nwork = states_only ? a.nseg - 1 : a.nseg, heads = a.B * a.H;
+    return {(int)(id % nwork), (int)((id / nwork) % heads), (int)(id / nwork / heads)};
+}
+__device__ __forceinline__ float *state_slot(const LaArgs &a, const Item &x, int seg)
+{
+    return a.ws + (((size_t)x.ip * a.B * a.H + x.bh) * a.nseg + seg) * kD * kD;
 }
 
 // STATES_ONLY: the segment's own state from zero goes to slot seg + 1 of the workspace; no
@@ -153,10 +213,8 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = (uint32_t)__cvta_generic_to_shared(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
-    const int seg = blockIdx.x % nwork;
-    const int bh = (blockIdx.x / nwork) % (a.B * a.H);
-    const int ip = blockIdx.x / nwork / (a.B * a.H);
+    const Item item = item_at(a, STATES_ONLY, blockIdx.x);
+    const int seg = item.seg, bh = item.bh, ip = item.ip;
     const LaPass &ps = a.pass[ip];
     const int b = bh / a.H, h = bh % a.H, rev = ps.rev;
     int t_lo, t_hi;
@@ -164,9 +222,15 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     const int n0 = t_lo / kC, nchunks = (t_hi + kC - 1) / kC - n0;
     const int c_last = t_hi - (n0 + nchunks - 1) * kC;          // tokens of the chunk at the segment's end in time
     auto chunk_at = [&](int it) { return n0 + (rev ? nchunks - 1 - it : it); };
-    auto tokens_of = [&](int n) { return n == n0 + nchunks - 1 ? c_last : kC; };
     auto bar = [&](int i) { return sb + SM_BAR + 8u * (uint32_t)i; };
-    float *slots = a.nseg > 1 ? a.ws + ((size_t)ip * a.B * a.H + bh) * a.nseg * kD * kD : nullptr;
+    // steps of the walk from three_at on keep all three parts of K'
+    int three_at = 0;
+    if (a.log_decay) {
+        const float fade = 6.f / (-1.4426950408889634f * a.log_decay[h]);       // tokens to 2^-6 (inf: never)
+        three_at = fade >= 0.f && fade < (float)(nchunks * kC) ? max(0, nchunks - 1 - (int)(fade / kC) - 1) : 0;
+    }
+    if (!STATES_ONLY && (seg != a.nseg - 1 || !ps.sT)) three_at = nchunks;
+    const int tail_at = c_last == kC ? -1 : rev ? 0 : nchunks - 1;      // the walk's step that is the ragged chunk
 
     // ---- set up: barriers, tensor memory, powers of lambda
     float *sWP = reinterpret_cast<float *>(smem + SM_WP), *sWK = reinterpret_cast<float *>(smem + SM_WK);
@@ -174,9 +238,10 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     if (tid == 0) {
         for (int i = 0; i < kBars; ++i) {
             const int count = (i >= FREE_K && i < FREE_V) ? (STATES_ONLY ? kKeyWarps : kKeyWarps + 1)
-                              : (i >= OUT_READY && i < KP_READY) || i == PV_GO || i == O_FREE ? kRowWarps
+                              : (i >= FREE_V && i < OUT_READY) ? (STATES_ONLY ? 1 : 2)
+                              : (i >= OUT_READY && i < U_READY) || i == PV_GO || i == O_FREE ? kRowWarps
                               : (i >= KP_READY && i < KP_FREE) ? kKeyWarps / 2
-                              : i == U_FREE || i == S0_READY ? kStateWarps : 1;
+                              : (i >= U_FREE && i < KP_READY) || i == S0_READY ? kStateWarps : 1;
             mbar_init(bar(i), (uint32_t)count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -197,12 +262,18 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid >= 2 * kC && tid < 2 * kC + 2) {
+        const double l = la_power(a.log_decay, h, tid == 2 * kC ? kC : c_last);
+        reinterpret_cast<float2 *>(smem + SM_LC)[tid - 2 * kC] = make_float2((float)l, (float)(l - (double)(float)l));
+    }
     if (tid < 2 * kC) {
         const int j = tid & (kC - 1), c = tid < kC ? kC : c_last;
         sWK[tid] = ps.f_write * sPW[rev ? j + 1 : max(c - 1 - j, 0)];
     }
     __syncthreads();
+    constexpr int kSlots = STATES_ONLY ? kKpSlotsStates : kKpSlots;
     constexpr uint32_t tm = 0;              // all 512 columns: they begin at 0
+    constexpr uint32_t id_nt = idesc_bf16(128, 128, 0, 0), id_nn = idesc_bf16(128, 128, 0, 1);
 
     bool ok = true;                         // false: a wait of this role ran out
     auto wait = [&](int i, uint32_t parity) {           // by one thread
@@ -225,7 +296,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
             const int i = 32 * warp + lane;
             const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
             for (int it = 0; it < nchunks; ++it) {
-                const int c = tokens_of(chunk_at(it)), st = it & 1;
+                const int c = it == tail_at ? c_last : kC, st = it & 1;
                 // ---- P from S
                 if (!wait_warp(S_READY, it)) break;
                 tc_fence_after();
@@ -262,17 +333,16 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 // ---- outputs through the q tile
                 if (!wait_warp(PV_DONE, it)) break;
                 tc_fence_after();
-                uint8_t *dst = smem + SM_Q + st * kTile + i * 128;
+                const uint32_t dst = sb + SM_Q + (uint32_t)(st * kTile + i * 128);
 #pragma unroll
                 for (int cb = 0; cb < 4; ++cb) {
                     float o[32];
                     tmem_ld32(row + TM_O + 32 * cb, o);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint4 u = make_uint4(pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
-                                                   pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
-                        *reinterpret_cast<uint4 *>(dst + (cb >> 1) * kHalf + (((4 * (cb & 1) + x) ^ (i & 7)) << 4)) = u;
-                    }
+                    for (int x = 0; x < 4; ++x)
+                        st_shared16(dst + (cb >> 1) * kHalf + (uint32_t)(((4 * (cb & 1) + x) ^ (i & 7)) << 4),
+                                    pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
+                                    pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
                 }
                 tc_fence_before();
                 proxy_fence();
@@ -286,7 +356,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     } else if (warp < kStateWarp0) {
         // ---- K'^T: slots of 16 tokens, this group's every second one; 32 key channels a warp
         const int quad = warp & 3, group = (warp - kRowWarps) >> 2;
-        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_KP;
+        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16);
         int slot = group, use = 0;                              // of the ring: every second one
         reg_dec<kKeyRegs>();
         // ldmatrix: lanes 8 m .. 8 m + 7 name the rows (tokens) of matrix m: tokens 8 (m / 2) ..,
@@ -296,7 +366,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         const uint32_t off0 = (uint32_t)((piece ^ jr) << 4), off1 = (uint32_t)(((piece + 2) ^ jr) << 4);
         for (int it = 0; it < nchunks; ++it) {
             const int st = it & 1;
-            const float *wk = sWK + (tokens_of(chunk_at(it)) != kC ? kC : 0) + 16 * group + 2 * (lane & 3);
+            const float *wk = sWK + (it == tail_at ? kC : 0) + 16 * group + 2 * (lane & 3);
             if (!wait_warp(FULL_K + st, it >> 1)) break;
 #pragma unroll 1
             for (int s4 = 0; s4 < 4; ++s4) {
@@ -306,25 +376,27 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 uint32_t k0[4], k1[4], hi[8], mid[8], lo[8];
                 ldmatrix4_trans(src + off0, k0);
                 ldmatrix4_trans(src + off1, k1);
+                const bool three = it >= three_at;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    cut3(k0[e], e < 2 ? w0 : w1, hi[e], mid[e], lo[e]);
-                    cut3(k1[e], e < 2 ? w0 : w1, hi[4 + e], mid[4 + e], lo[4 + e]);
+                for (int e = 0; e < 8; ++e) {
+                    const float2 x = scale_pair(e < 4 ? k0[e & 3] : k1[e & 3], (e & 2) ? w1 : w0);
+                    if (three) cut3(x, hi[e], mid[e], lo[e]);
+                    else split_pair2(x, hi[e], mid[e]);
                 }
                 if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int e = 0; e < 8; e += 4) {
-                    const uint32_t dst = row + ((uint32_t)(4 * e) << 16) + slot * kKpSlot;
+                    const uint32_t dst = row + ((uint32_t)(4 * e) << 16) + kp_column(slot);
                     tmem_st_16x8(dst, hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
                     tmem_st_16x8(dst + kKpPart, mid[e], mid[e + 1], mid[e + 2], mid[e + 3]);
-                    tmem_st_16x8(dst + 2 * kKpPart, lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
+                    if (three) tmem_st_16x8(dst + 2 * kKpPart, lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(KP_READY + slot);
                 slot += 2;
-                if (slot >= kKpSlots) { slot -= kKpSlots; ++use; }
+                if (slot >= kSlots) { slot -= kSlots; ++use; }
             }
             if (!ok) break;
             arrive_warp(FREE_K + st);
@@ -333,69 +405,66 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         // ---- the state: key channel r, value columns 64 part ..
         const int quad = warp & 3, part = (warp - kStateWarp0) >> 2;
         const int r = 32 * quad + lane;
-        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_U + 64 * part;
+        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + 64 * part;
         reg_inc<kStateRegs>();
         float S[64];
         {
-            const float *s0 = STATES_ONLY ? nullptr : slots ? slots + (size_t)seg * kD * kD
+            const float *s0 = STATES_ONLY ? nullptr : a.nseg > 1 ? state_slot(a, item, seg)
                               : ps.s0 ? ps.s0 + (size_t)bh * kD * kD : nullptr;
             if (!s0) {
 #pragma unroll
                 for (int x = 0; x < 64; ++x) S[x] = 0.f;
-            } else if (!slots && ps.s0_transposed) {
+            } else if (a.nseg == 1 && ps.s0_transposed) {
 #pragma unroll
                 for (int x = 0; x < 64; ++x) S[x] = s0[(64 * part + x) * kD + r];
             } else {
 #pragma unroll
-                for (int x = 0; x < 64; x += 4)
-                    *reinterpret_cast<float4 *>(&S[x]) = *reinterpret_cast<const float4 *>(s0 + r * kD + 64 * part + x);
+                for (int x = 0; x < 64; x += 4) {
+                    const float4 u = *reinterpret_cast<const float4 *>(s0 + r * kD + 64 * part + x);
+                    S[x] = u.x; S[x + 1] = u.y; S[x + 2] = u.z; S[x + 3] = u.w;
+                }
             }
         }
-        uint8_t *sS0 = smem + SM_S0 + part * kHalf + r * 128;
+        const uint32_t s0_row = sb + SM_S0 + part * kHalf + (uint32_t)(r * 128), s0_swz = (uint32_t)(r & 7) << 4;
         auto publish = [&] {                                    // the state as the operand of Q S0
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                *reinterpret_cast<uint4 *>(sS0 + ((x ^ (r & 7)) << 4)) =
-                    make_uint4(pack_bf16(S[8 * x], S[8 * x + 1]), pack_bf16(S[8 * x + 2], S[8 * x + 3]),
-                               pack_bf16(S[8 * x + 4], S[8 * x + 5]), pack_bf16(S[8 * x + 6], S[8 * x + 7]));
+                st_shared16(s0_row + ((16u * (uint32_t)x) ^ s0_swz), pack_bf16(S[8 * x], S[8 * x + 1]),
+                            pack_bf16(S[8 * x + 2], S[8 * x + 3]), pack_bf16(S[8 * x + 4], S[8 * x + 5]),
+                            pack_bf16(S[8 * x + 6], S[8 * x + 7]));
             proxy_fence();
             arrive_warp(S0_READY);
         };
         if (!STATES_ONLY) publish();
-        const double whole = la_power(a.log_decay, h, kC), ragged = la_power(a.log_decay, h, c_last);
-        const float2 l_whole = make_float2((float)whole, (float)(whole - (double)(float)whole));
-        const float2 l_ragged = make_float2((float)ragged, (float)(ragged - (double)(float)ragged));
         for (int it = 0; it < nchunks; ++it) {
             // S <- lambda^c S + U
-            if (!wait_warp(U_READY, it)) break;
+            const int ub = STATES_ONLY ? it & 1 : 0;
+            if (!wait_warp(U_READY + ub, STATES_ONLY ? it >> 1 : it)) break;
             tc_fence_after();
-            const float2 l = tokens_of(chunk_at(it)) != kC ? l_ragged : l_whole;
-            const float2 lh = make_float2(l.x, l.x), ll = make_float2(l.y, l.y);
+            const float2 l = reinterpret_cast<const float2 *>(smem + SM_LC)[it == tail_at];
 #pragma unroll
-            for (int x = 0; x < 64; x += 16) {
-                float u[16];
-                tmem_ld16(row + x, u);
+            for (int x = 0; x < 64; x += 8) {
+                float u[8];
+                tmem_ld8(row + (ub ? TM_O : TM_U) + x, u);
 #pragma unroll
-                for (int y = 0; y < 16; y += 2) {
-                    const float2 s = make_float2(S[x + y], S[x + y + 1]);
-                    const float2 n = fma2(lh, s, fma2(ll, s, make_float2(u[y], u[y + 1])));
-                    S[x + y] = n.x;
-                    S[x + y + 1] = n.y;
-                }
+                for (int y = 0; y < 8; ++y) S[x + y] = fmaf(l.x, S[x + y], fmaf(l.y, S[x + y], u[y]));
             }
             tc_fence_before();
-            arrive_warp(U_FREE);
+            arrive_warp(U_FREE + ub);
             if (!STATES_ONLY && it + 1 < nchunks) {
                 if (!wait_warp(QS_READY, it)) break;            // the operand of this chunk has been read
                 publish();
             }
         }
-        float *dst = STATES_ONLY ? slots + (size_t)(seg + 1) * kD * kD
-                     : (seg == a.nseg - 1 && ps.sT) ? ps.sT + (size_t)bh * kD * kD : nullptr;
+        unsigned int id;                        // read again: the loop has no register for what follows from it
+        asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(id));
+        const Item end = item_at(a, STATES_ONLY, id);
+        float *dst = STATES_ONLY ? state_slot(a, end, end.seg + 1)
+                     : (end.seg == a.nseg - 1 && a.pass[end.ip].sT) ? a.pass[end.ip].sT + (size_t)end.bh * kD * kD : nullptr;
         if (dst && ok)
 #pragma unroll
             for (int x = 0; x < 64; x += 4)
-                *reinterpret_cast<float4 *>(dst + r * kD + 64 * part + x) = *reinterpret_cast<const float4 *>(&S[x]);
+                *reinterpret_cast<float4 *>(dst + r * kD + 64 * part + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
     } else if (warp == kTmaWarp) {
         if (lane == 0) {
             auto load = [&](const CUtensorMap *m, uint32_t dst, int full, int n) {
@@ -439,50 +508,27 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     if (!STATES_ONLY) mbar_wait(bar(FULL_Q + (it & 1)), (it >> 1) & 1);
                 }
         }
-    } else {
-        // The whole warp walks the loop and one elected lane issues, so that descriptors stay in
+    } else if (warp == kMmaWarp) {
+        // Whole warps walk the loops and one elected lane issues, so that descriptors stay in
         // uniform registers: under `lane == 0` each product took 100 cycles to issue, against
         // the 64 it runs.
-        constexpr uint32_t id_nt = idesc_bf16(128, 128, 0, 0), id_nn = idesc_bf16(128, 128, 0, 1);
-        const uint64_t dq = desc_sw128(sb + SM_Q, 16), dk = desc_sw128(sb + SM_K, 16), dv = desc_sw128(sb + SM_V, kHalf);
-        const uint64_t ds = desc_sw128(sb + SM_S0, kHalf);
-        // A K step of 16 channels is 32 bytes inside the swizzled rows of a K-major tile, 16 rows
-        // of an MN-major one (addresses in 16 bytes).
-        auto k_major = [](int ks) { return (uint64_t)((ks >> 2) * (kHalf >> 4) + (ks & 3) * 2); };
-        int slot = 0, use = 0;
-        // U (+)= K'^T V over 64 tokens: a K step of three parts per slot
-        auto update = [&](uint64_t v, int half) {
-#pragma unroll
-            for (int ks = 4 * half; ks < 4 * half + 4; ++ks) {
-                if (!wait_warp(KP_READY + slot, use)) return false;
-                tc_fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int p = 0; p < 3; ++p)
-                        umma_bf16_ta(tm + TM_U, tm + TM_KP + slot * kKpSlot + p * kKpPart, v + (uint64_t)(ks * 128), id_nn,
-                                     ks > 0 || p > 0);
-                    umma_commit(bar(KP_FREE + slot));
-                    if (ks == 7) umma_commit(bar(U_READY));
-                }
-                if (++slot == kKpSlots) { slot = 0; ++use; }
-            }
-            return true;
-        };
-        for (int it = 0; it < nchunks; ++it) {
-            const int st = it & 1;
-            const uint64_t q = dq + (uint64_t)(st * (kTile >> 4)), k = dk + (uint64_t)(st * (kTile >> 4));
-            const uint64_t v = dv + (uint64_t)(st * (kTile >> 4));
-            if (!wait_warp(FULL_V + st, it >> 1)) break;
-            if (it > 0 && !wait_warp(U_FREE, it - 1)) break;
-            if (!update(v, 0)) break;
-            if (!STATES_ONLY) {
+        if (!STATES_ONLY) {
+            const uint32_t dq = desc_lo(sb + SM_Q, 16), dk = desc_lo(sb + SM_K, 16);
+            const uint32_t dv = desc_lo(sb + SM_V, kHalf), ds = desc_lo(sb + SM_S0, kHalf);
+            // A K step of 16 channels is 32 bytes inside the swizzled rows of a K-major tile, 16
+            // rows of an MN-major one (addresses in 16 bytes).
+            auto k_major = [](int ks) { return (uint32_t)((ks >> 2) * (kHalf >> 4) + (ks & 3) * 2); };
+            for (int it = 0; it < nchunks; ++it) {
+                const int st = it & 1;
+                const uint32_t stage = (uint32_t)st * (kTile >> 4);
                 // S = Q K^T
                 if (!wait_warp(FULL_Q + st, it >> 1) || !wait_warp(FULL_K + st, it >> 1)) break;
                 if (it > 0 && !wait_warp(PV_DONE, it - 1)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) umma_bf16(tm + TM_S, q + k_major(ks), k + k_major(ks), id_nt, ks > 0);
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_ss(tm + TM_S, dq + stage + k_major(ks), dk + stage + k_major(ks), id_nt, ks > 0);
                     umma_commit(bar(S_READY));
                     umma_commit(bar(FREE_K + st));
                 }
@@ -491,23 +537,52 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) umma_bf16(tm + TM_O, q + k_major(ks), ds + (uint64_t)(ks * 128), id_nn, ks > 0);
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_ss(tm + TM_O, dq + stage + k_major(ks), ds + (uint32_t)(ks * 128), id_nn, ks > 0);
                     umma_commit(bar(QS_READY));
                 }
-            }
-            if (!update(v, 1)) break;
-            if (!STATES_ONLY) {
                 // O += P V
-                if (!wait_warp(PV_GO, it)) break;
+                if (!wait_warp(FULL_V + st, it >> 1) || !wait_warp(PV_GO, it)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16_ta(tm + TM_O, tm + TM_P + 8 * ks, v + (uint64_t)(ks * 128), id_nn, 1);
+                        umma_ts(tm + TM_O, tm + TM_P + 8 * ks, dv + stage + (uint32_t)(ks * 128), id_nn, true);
                     umma_commit(bar(PV_DONE));
                     umma_commit(bar(FREE_V + st));
                 }
-            } else if (elect_one()) umma_commit(bar(FREE_V + st));
+            }
+        }
+    } else {
+        // U = K'^T V: a K step of three parts per slot
+        const uint32_t dv = desc_lo(sb + SM_V, kHalf);
+        int slot = 0, use = 0;
+        for (int it = 0; it < nchunks; ++it) {
+            const int st = it & 1;
+            const uint32_t v = dv + (uint32_t)st * (kTile >> 4);
+            if (!wait_warp(FULL_V + st, it >> 1)) break;
+            const int ub = STATES_ONLY ? it & 1 : 0;
+            const uint32_t u = tm + (ub ? TM_O : TM_U);
+            if (STATES_ONLY ? it >= 2 && !wait_warp(U_FREE + ub, (it >> 1) - 1) : it > 0 && !wait_warp(U_FREE, it - 1)) break;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                if (!wait_warp(KP_READY + slot, use)) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        if (p < 2 || it >= three_at)
+                            umma_ts(u, tm + kp_column(slot) + p * kKpPart, v + (uint32_t)(ks * 128), id_nn,
+                                    ks > 0 || p > 0);
+                    umma_commit(bar(KP_FREE + slot));
+                    if (ks == 7) {
+                        umma_commit(bar(U_READY + ub));
+                        umma_commit(bar(FREE_V + st));
+                    }
+                }
+                if (++slot == kSlots) { slot = 0; ++use; }
+            }
+            if (!ok) break;
         }
     }
     __syncwarp();
@@ -554,6 +629,13 @@ cudaError_t token_map(const LaArgs &a, const void *p, CUtensorMap *m)
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+template <typename Kernel>
+int launch_registers(Kernel kernel)
+{
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : -1;
+}
+
 }  // namespace
 
 bool la_tc_supported(int dk, int dv, kda_dtype dtype) { return dtype == KDA_BF16 && dk == kD && dv == kD; }
@@ -570,12 +652,11 @@ cudaError_t launch_la_tc(const LaArgs &a, bool states_only, cudaStream_t stream)
     }
     if (e != cudaSuccess) return e;
     auto kernel = states_only ? la_tc_kernel<true> : la_tc_kernel<false>;
-    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM_TOTAL)) != cudaSuccess)
-        return e;
     // the move of registers between warps is sized for this many: with fewer it would wait for ever
-    cudaFuncAttributes attr;
-    if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
-    if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    static const int regs[2] = {launch_registers(la_tc_kernel<false>), launch_registers(la_tc_kernel<true>)};
+    if (regs[states_only] != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    static OncePerDevice once[2];
+    if ((e = set_shared_memory(kernel, (int)SM_TOTAL, once[states_only])) != cudaSuccess) return e;
     const size_t grid = (size_t)a.npass * a.B * a.H * (states_only ? a.nseg - 1 : a.nseg);
     kernel<<<(unsigned)grid, kThreads, SM_TOTAL, stream>>>(a, maps);
     e = cudaGetLastError();

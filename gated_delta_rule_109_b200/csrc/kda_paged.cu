@@ -391,7 +391,8 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
 {
     using L = PagedSmem<D, InT, HG>;
     auto kernel = paged_decode_kernel<D, InT, HG>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total);
+    static OncePerDevice once;
+    cudaError_t e = set_shared_memory(kernel, L::total, once);
     if (e != cudaSuccess) return e;
     const unsigned int grid = kSms * resident<D, InT, HG>();
     cudaLaunchConfig_t cfg = {};
