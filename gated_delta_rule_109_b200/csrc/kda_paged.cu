@@ -1,11 +1,20 @@
-// Paged decode attention on CUDA cores (the split of the work is in kda_paged.cuh).
+// Paged decode attention (the split of the work is in kda_paged.cuh).
 //
 // A CTA is four warps; of every unit of 64 keys a warp takes 16 and keeps its own running
 // maximum, sum and output, so that the warps meet only at the end of a stretch.  Each warp
 // moves its keys and values through its own ring of shared-memory slots with 16-byte
-// asynchronous copies, kStages - 1 units ahead.  Scores: lane = (key, half of the
-// channels), the query broadcast from shared memory.  Output: lane = D / 32 channels, the
-// probabilities broadcast.  Sums and statistics are fp32.
+// asynchronous copies, kStages - 1 units ahead, and looks the page of its next unit up one
+// unit before that.  Reading the cache is what bounds it: every key and value is read once
+// for all query heads of its group.
+//
+// bf16: the products are warp matrix instructions with the keys as rows, S^T = K q^T and
+// O^T = V^T P^T, so that the 8 columns are query heads and a group of fewer than 8 wastes
+// little (with the heads as rows it would be 16).  There is one query per sequence: at most
+// some 40 flops per byte, far from what tcgen05's 128-row tiles are for.  P is split into two
+// bf16 parts, which leaves the rounding of the output as the only one of that size.
+// fp32: CUDA cores.  Scores: lane = (key, half of the channels), the query broadcast from
+// shared memory.  Output: lane = D / 32 channels, the probabilities broadcast.
+// Sums and statistics are fp32 in both.
 #include <math.h>
 
 #include "kda_la.cuh"
@@ -18,7 +27,7 @@ __device__ unsigned int g_paged_status = 0;
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps, kWarpKeys = kPagedTile / kWarps, kStages = 3;
-constexpr int kSms = 148;
+constexpr int kSms = 148, kMaxResident = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real)
@@ -28,6 +37,17 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool real)
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// t / d and t % d for 0 <= t < 2^31 by multiplication: with 2^l >= d > 2^(l-1) and
+// m = floor(2^32 (2^l - d) / d) + 1 the quotient is (m t / 2^32 + t) / 2^l.
+struct Divider { unsigned int m, l, d; };
+Divider divider(unsigned int d)
+{
+    unsigned int l = 0;
+    while ((1ull << l) < d) ++l;
+    return {(unsigned int)(((1ull << 32) * ((1ull << l) - d)) / d + 1), l, d};
+}
+__device__ __forceinline__ unsigned int quotient(unsigned int t, const Divider &x) { return (__umulhi(x.m, t) + t) >> x.l; }
 
 // Keys that row b attends to; -1 for a row that is left alone (idle, or longer than its table).
 __device__ __forceinline__ int row_keys(const PagedArgs &a, int b)
@@ -91,30 +111,254 @@ __device__ __forceinline__ RowAt find_row(const PagedArgs &a, unsigned long long
     return r;
 }
 
+// ---- warp matrix instructions (bf16, fp32 accumulators)
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t saddr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t saddr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(saddr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
 template <int D, typename InT, int HG>
 struct PagedSmem {
+    static constexpr bool mma = sizeof(InT) == 2;
     static constexpr int row = D * (int)sizeof(InT) + 16;                 // bytes; rows 4 banks apart
     static constexpr int slot = 2 * kWarpKeys * row;                      // K rows, then V rows
     static constexpr int ring = kWarps * kStages * slot;
-    static constexpr int off_q = ring;                                    // [HG][D] fp32, scaled by scale log2 e
-    static constexpr int off_p = off_q + HG * D * 4;                      // [warp][HG][16]
-    static constexpr int off_ml = off_p + kWarps * HG * kWarpKeys * 4;    // [warp][HG] maximum, sum
+    static constexpr int off_q = ring;                                    // fp32: [HG][D], scaled by scale log2 e
+    static constexpr int off_p = off_q + (mma ? 0 : HG * D * 4);          // fp32: [warp][HG][16]
+    static constexpr int off_ml = off_p + (mma ? 0 : kWarps * HG * kWarpKeys * 4);    // [warp][HG] maximum, sum
     static constexpr int total = off_ml + kWarps * HG * 8;
     static_assert(kWarps * HG * D * 4 <= ring, "the warps' outputs meet in the ring");
 };
 
+// The running maximum, sum and output of HG query heads over a warp's keys.  Lane's share:
+// bf16: heads 2 (lane % 4) + {0, 1} + 8 n of n-tile n; output channels lane / 4 + 8 x;
+// fp32: all heads; the sum of key lane (of the first 16), output channels DL lane ...
+template <int D, int HG>
+struct MmaState {
+    static constexpr int NT = HG / 8, KS = D / 16;
+    uint32_t q[NT][KS][2];
+    float m[NT][2], l[NT][2], o[NT][KS][4];
+
+    __device__ __forceinline__ void start(const __nv_bfloat16 *qh, int nh, int lane)
+    {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int head = 8 * n + (lane >> 2);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    q[n][ks][x] = head < nh ? *reinterpret_cast<const uint32_t *>(qh + head * D + 16 * ks + 8 * x + 2 * (lane & 3)) : 0u;
+                    o[n][ks][2 * x] = o[n][ks][2 * x + 1] = 0.f;
+                }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) { m[n][x] = -INFINITY; l[n][x] = 0.f; }
+        }
+    }
+    // 16 keys of which `seen` (one bit a key) count; scores in units of log 2 after `scale`
+    __device__ __forceinline__ void step(uint32_t k, uint32_t v, int row, unsigned int seen, float scale, int lane)
+    {
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
+        const uint32_t ka = k + (uint32_t)(((lane & 7) + 8 * ((lane >> 3) & 1)) * row + 16 * (lane >> 4));
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a[4];
+            ldsm4(ka + 32 * ks, a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(s[n], a, q[n][ks][0], q[n][ks][1]);
+        }
+        const bool on0 = (seen >> (lane >> 2)) & 1u, on1 = (seen >> ((lane >> 2) + 8)) & 1u;
+        uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float p[4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float s0 = on0 ? s[n][x] * scale : -INFINITY, s1 = on1 ? s[n][2 + x] * scale : -INFINITY;
+                float top = fmaxf(s0, s1);
+                if (__any_sync(0xffffffffu, top > m[n][x])) {           // a running maximum rises
+#pragma unroll
+                    for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+                    top = fmaxf(top, m[n][x]);
+                    // -inf before and after: no key yet, nothing to rescale
+                    const float f = m[n][x] == -INFINITY ? 0.f : exp2f(m[n][x] - top);
+                    m[n][x] = top;
+                    l[n][x] *= f;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) { o[n][ks][x] *= f; o[n][ks][2 + x] *= f; }
+                }
+                const float base = m[n][x] == -INFINITY ? 0.f : m[n][x];
+                p[x] = on0 ? exp2f(s0 - base) : 0.f;
+                p[2 + x] = on1 ? exp2f(s1 - base) : 0.f;
+                l[n][x] += p[x] + p[2 + x];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * x], p[2 * x + 1]);
+                const float2 f = __bfloat1622float2(h);
+                const __nv_bfloat162 r = __floats2bfloat162_rn(p[2 * x] - f.x, p[2 * x + 1] - f.y);
+                hi[n][x] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
+                lo[n][x] = transpose8x8(*reinterpret_cast<const uint32_t *>(&r));
+            }
+        }
+        const uint32_t va = v + (uint32_t)(((lane & 7) + 8 * (lane >> 4)) * row + 16 * ((lane >> 3) & 1));
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t a[4];
+            ldsm4_trans(va + 32 * ks, a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma16816(o[n][ks], a, hi[n][0], hi[n][1]);
+                mma16816(o[n][ks], a, lo[n][0], lo[n][1]);
+            }
+        }
+    }
+    __device__ __forceinline__ void finish(float *sO, float *sML, int lane)
+    {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int head = 8 * n + 2 * (lane & 3) + x;
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], y);
+                if (lane < 4) {
+                    sML[2 * head] = m[n][x];
+                    sML[2 * head + 1] = l[n][x];
+                }
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    sO[head * D + 16 * ks + (lane >> 2)] = o[n][ks][x];
+                    sO[head * D + 16 * ks + 8 + (lane >> 2)] = o[n][ks][2 + x];
+                }
+            }
+    }
+};
+
+template <int D, int HG>
+struct SimtState {
+    static constexpr int DL = D / 32;
+    float m[HG], l[HG], o[HG][DL];
+
+    __device__ __forceinline__ void start()
+    {
+#pragma unroll
+        for (int g = 0; g < HG; ++g) {
+            m[g] = -INFINITY;
+            l[g] = 0.f;
+#pragma unroll
+            for (int x = 0; x < DL; ++x) o[g][x] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void step(const uint8_t *k, const uint8_t *v, int row, unsigned int seen, const float *sQ,
+                                         float *sP, int lane)
+    {
+        float s[HG];
+#pragma unroll
+        for (int g = 0; g < HG; ++g) s[g] = 0.f;
+        const float *kr = reinterpret_cast<const float *>(k + (lane & 15) * row) + (lane >> 4) * (D / 2);
+        const float *qh = sQ + (lane >> 4) * (D / 2);
+#pragma unroll 4
+        for (int d = 0; d < D / 2; d += 4) {
+            const float4 kk = la_load4(kr + d);
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+                const float4 qq = la_load4(qh + g * D + d);
+                s[g] += kk.x * qq.x; s[g] += kk.y * qq.y; s[g] += kk.z * qq.z; s[g] += kk.w * qq.w;
+            }
+        }
+        const bool on = (seen >> (lane & 15)) & 1u;
+#pragma unroll
+        for (int g = 0; g < HG; ++g) {
+            s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
+            if (!on) s[g] = -INFINITY;
+            if (__any_sync(0xffffffffu, s[g] > m[g])) {         // the running maximum rises
+                float top = s[g];
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                top = fmaxf(top, m[g]);
+                const float f = exp2f(m[g] - top);              // exp2(-inf) = 0 the first time
+                l[g] *= f;
+#pragma unroll
+                for (int x = 0; x < DL; ++x) o[g][x] *= f;
+                m[g] = top;
+            }
+            // a maximum of -inf: every score so far is -inf, each weighs nothing
+            const float p = on ? exp2f(s[g] - (m[g] == -INFINITY ? 0.f : m[g])) : 0.f;
+            if (lane < 16) {
+                l[g] += p;
+                sP[g * kWarpKeys + lane] = p;
+            }
+        }
+        __syncwarp();
+        const uint8_t *vr = v + 4 * DL * lane;
+#pragma unroll
+        for (int j = 0; j < kWarpKeys; j += 4) {
+            float x[4][DL];
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                for (int y = 0; y < DL; ++y) x[jj][y] = reinterpret_cast<const float *>(vr + (j + jj) * row)[y];
+#pragma unroll
+            for (int g = 0; g < HG; ++g) {
+                const float4 p = la_load4(sP + g * kWarpKeys + j);
+#pragma unroll
+                for (int y = 0; y < DL; ++y) {
+                    o[g][y] += p.x * x[0][y]; o[g][y] += p.y * x[1][y];
+                    o[g][y] += p.z * x[2][y]; o[g][y] += p.w * x[3][y];
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void finish(float *sO, float *sML, int lane)
+    {
+#pragma unroll
+        for (int g = 0; g < HG; ++g) {
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], x);
+            if (lane == 0) {
+                sML[2 * g] = m[g];
+                sML[2 * g + 1] = l[g];
+            }
+#pragma unroll
+            for (int x = 0; x < DL; ++x) sO[g * D + DL * lane + x] = o[g][x];
+        }
+    }
+};
+
 template <int D, typename InT, int HG>
 __global__ void __launch_bounds__(kThreads)
-paged_decode_kernel(const __grid_constant__ PagedArgs a)
+paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
 {
     using L = PagedSmem<D, InT, HG>;
     constexpr int CPR = D * (int)sizeof(InT) / 16;      // 16-byte pieces of a row
-    constexpr int DL = D / 32;                          // output channels of a lane
+    constexpr int RPI = 32 / CPR;                       // rows that a warp's copy instruction covers
+    static_assert(CPR <= 32 && 32 % CPR == 0, "pieces");
     extern __shared__ __align__(16) uint8_t smem[];
-    const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float *sQ = reinterpret_cast<float *>(smem + L::off_q);
-    float *sP = reinterpret_cast<float *>(smem + L::off_p) + warp * HG * kWarpKeys;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)(warp * kStages * L::slot);
     float *sML = reinterpret_cast<float *>(smem + L::off_ml);
     float *sO = reinterpret_cast<float *>(smem);
 
@@ -131,7 +375,6 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
 
     int b = at.b, part = 0;
     unsigned long long row_first = at.first;
-    const InT *kc = static_cast<const InT *>(a.k_cache), *vc = static_cast<const InT *>(a.v_cache);
     while (u < u1) {
         int n = row_keys(a, b), tiles = (max(n, 0) + kPagedTile - 1) / kPagedTile;
         while (u >= row_first + per * tiles) {          // next row that has units
@@ -145,140 +388,96 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
         const int tile1 = (int)min((unsigned long long)tiles, (unsigned long long)tile0 + (u1 - u));
         const bool whole = tile0 == 0 && tile1 == tiles;
         const int new_at = a.k ? n - 1 : -1;
+        const int *table = a.block_table + (size_t)b * a.max_pages;
 
-        __syncthreads();                                // the stretch before is written out
-        for (int e = tid; e < HG * D; e += kThreads)
-            sQ[e] = e / D < nh ? to_f32(static_cast<const InT *>(a.q)[((size_t)b * a.H + h0) * D + e]) * (a.scale * kLog2e)
-                               : 0.f;
-        __syncthreads();
-
-        // One slot of this warp's ring: 16 keys and values from key t on; masked rows are zeros.
-        auto fetch = [&](int tile) {
-            const int t = tile * kPagedTile + warp * kWarpKeys + (lane & 15);
-            const InT *kp = kc, *vp = vc;
-            bool real = tile < tile1 && t < n;
-            if (real) {
-                const int page = a.block_table[(size_t)b * a.max_pages + t / a.page_size];
-                const bool good = page >= 0 && page < a.num_pages;
-                if (!good) atomicOr(&g_paged_status, 1u);
-                const size_t at_cache = (((size_t)(good ? page : 0) * a.page_size + t % a.page_size) * a.Hkv + hk) * D;
-                if (t == new_at) {
-                    kp = static_cast<const InT *>(a.k) + ((size_t)b * a.Hkv + hk) * D;
-                    vp = static_cast<const InT *>(a.v) + ((size_t)b * a.Hkv + hk) * D;
-                } else {
-                    kp += at_cache;
-                    vp += at_cache;
-                    real = good;
-                }
-            }
-            const uint32_t dst = sbase + (uint32_t)((warp * kStages + tile % kStages) * L::slot);
-            const unsigned long long kpi = reinterpret_cast<unsigned long long>(kp), vpi = reinterpret_cast<unsigned long long>(vp);
-#pragma unroll
-            for (int e = 0; e < kWarpKeys * CPR / 32; ++e) {
-                const int id = e * 32 + lane, r = id / CPR, c = id % CPR;
-                const bool ok = __shfl_sync(0xffffffffu, real, r);
-                const uint8_t *ks = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, kpi, r)) + 16 * c;
-                const uint8_t *vs = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, vpi, r)) + 16 * c;
-                cp16(dst + (uint32_t)(r * L::row + 16 * c), ok ? ks : reinterpret_cast<const uint8_t *>(kc), ok);
-                cp16(dst + (uint32_t)((kWarpKeys + r) * L::row + 16 * c), ok ? vs : reinterpret_cast<const uint8_t *>(vc), ok);
-            }
+        // Page of this lane's key of a unit: key lane % 16 of the warp's 16 (-1: none).
+        auto key_of = [&](int tile) { return tile * kPagedTile + warp * kWarpKeys + (lane & 15); };
+        auto page_of = [&](int tile) {
+            const int t = key_of(tile);
+            return tile < tile1 && t < n ? table[quotient((unsigned int)t, by_page)] : -1;
         };
-        // a key counts if it is one of the row's and its page is in the cache
-        auto counts = [&](int t) {
-            if (t >= n) return false;
-            if (t == new_at) return true;
-            const int page = a.block_table[(size_t)b * a.max_pages + t / a.page_size];
-            return page >= 0 && page < a.num_pages;
+        // One slot of this warp's ring; rows that do not count are zeros and nothing is read for
+        // them.  Returns a bit for each key that counts.
+        auto fetch = [&](int tile, int page) {
+            const int t = key_of(tile);
+            const bool mine = tile < tile1 && t < n, is_new = mine && t == new_at;
+            const bool good = page >= 0 && page < a.num_pages;
+            if (mine && !good) atomicOr(&g_paged_status, 1u);
+            const bool real = is_new || (mine && good);
+            const InT *kp = static_cast<const InT *>(a.k_cache), *vp = static_cast<const InT *>(a.v_cache);
+            if (is_new) {
+                kp = static_cast<const InT *>(a.k) + ((size_t)b * a.Hkv + hk) * D;
+                vp = static_cast<const InT *>(a.v) + ((size_t)b * a.Hkv + hk) * D;
+            } else if (real) {
+                const size_t off = (((size_t)page * a.page_size + ((unsigned int)t - quotient((unsigned int)t, by_page) * by_page.d)) *
+                                        a.Hkv + hk) * D;
+                kp += off;
+                vp += off;
+            }
+            const unsigned int seen = __ballot_sync(0xffffffffu, real) & 0xffffu;
+            const uint32_t dst = ring + (uint32_t)((tile % kStages) * L::slot + (lane / CPR) * L::row + 16 * (lane % CPR));
+            const unsigned long long kpi = reinterpret_cast<unsigned long long>(kp) , vpi = reinterpret_cast<unsigned long long>(vp);
+#pragma unroll
+            for (int e = 0; e < kWarpKeys / RPI; ++e) {
+                const int r = e * RPI + lane / CPR;
+                const bool ok = (seen >> r) & 1u;
+                const unsigned long long ks = __shfl_sync(0xffffffffu, kpi, r), vs = __shfl_sync(0xffffffffu, vpi, r);
+                cp16(dst + (uint32_t)(e * RPI * L::row), reinterpret_cast<const uint8_t *>(ks) + 16 * (lane % CPR), ok);
+                cp16(dst + (uint32_t)((kWarpKeys + e * RPI) * L::row), reinterpret_cast<const uint8_t *>(vs) + 16 * (lane % CPR), ok);
+            }
+            cp_commit();
+            return seen;
         };
 
-        float m[HG], l[HG], o[HG][DL];
-#pragma unroll
-        for (int g = 0; g < HG; ++g) {
-            m[g] = -INFINITY;
-            l[g] = 0.f;
-#pragma unroll
-            for (int x = 0; x < DL; ++x) o[g][x] = 0.f;
-        }
-#pragma unroll
-        for (int st = 0; st < kStages - 1; ++st) {
-            fetch(tile0 + st);
-            cp_commit();
-        }
-        for (int tile = tile0; tile < tile1; ++tile) {
-            fetch(tile + kStages - 1);
-            cp_commit();
-            cp_wait<kStages - 1>();
-            __syncwarp();
-            const uint8_t *slot = smem + (warp * kStages + tile % kStages) * L::slot;
-            const int t = tile * kPagedTile + warp * kWarpKeys + (lane & 15);
-            // ---- scores of key lane & 15, channels split between the half-warps
-            float s[HG];
-#pragma unroll
-            for (int g = 0; g < HG; ++g) s[g] = 0.f;
-            const InT *kr = reinterpret_cast<const InT *>(slot + (lane & 15) * L::row) + (lane >> 4) * (D / 2);
-            const float *qh = sQ + (lane >> 4) * (D / 2);
-#pragma unroll 4
-            for (int d = 0; d < D / 2; d += 4) {
-                const float4 kk = la_load4(kr + d);
-#pragma unroll
-                for (int g = 0; g < HG; ++g) {
-                    const float4 qq = la_load4(qh + g * D + d);
-                    s[g] += kk.x * qq.x; s[g] += kk.y * qq.y; s[g] += kk.z * qq.z; s[g] += kk.w * qq.w;
-                }
+        static_assert(kStages == 3, "two units ahead");
+        unsigned int seen0 = fetch(tile0, page_of(tile0)), seen1 = fetch(tile0 + 1, page_of(tile0 + 1)), seen2;
+        int page2 = page_of(tile0 + 2);
+        const InT *qh = static_cast<const InT *>(a.q) + ((size_t)b * a.H + h0) * D;
+        if constexpr (L::mma) {
+            MmaState<D, HG> st;
+            st.start(qh, nh, lane);
+            for (int tile = tile0; tile < tile1; ++tile) {
+                seen2 = fetch(tile + 2, page2);
+                page2 = page_of(tile + 3);
+                cp_wait<2>();
+                __syncwarp();
+                const uint32_t k = ring + (uint32_t)((tile % kStages) * L::slot);
+                st.step(k, k + kWarpKeys * L::row, L::row, seen0, a.scale * kLog2e, lane);
+                seen0 = seen1;
+                seen1 = seen2;
+                __syncwarp();                           // the slot is free again
             }
-            const bool seen = counts(t);
-#pragma unroll
-            for (int g = 0; g < HG; ++g) {
-                s[g] += __shfl_xor_sync(0xffffffffu, s[g], 16);
-                if (!seen) s[g] = -INFINITY;
-                if (__any_sync(0xffffffffu, s[g] > m[g])) {     // the running maximum rises
-                    float top = s[g];
-#pragma unroll
-                    for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    top = fmaxf(top, m[g]);
-                    const float f = exp2f(m[g] - top);          // exp2(-inf) = 0 the first time
-                    l[g] *= f;
-#pragma unroll
-                    for (int x = 0; x < DL; ++x) o[g][x] *= f;
-                    m[g] = top;
-                }
-                // a maximum of -inf: every score so far is -inf, each weighs nothing
-                const float p = seen ? exp2f(s[g] - (m[g] == -INFINITY ? 0.f : m[g])) : 0.f;
-                if (lane < 16) {
-                    l[g] += p;
-                    sP[g * kWarpKeys + lane] = p;
-                }
+            cp_wait<0>();
+            __syncthreads();
+            st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
+        } else {
+            float *sQ = reinterpret_cast<float *>(smem + L::off_q);
+            float *sP = reinterpret_cast<float *>(smem + L::off_p) + warp * HG * kWarpKeys;
+            for (int e = tid; e < HG * D; e += kThreads) sQ[e] = e / D < nh ? to_f32(qh[e]) * (a.scale * kLog2e) : 0.f;
+            __syncthreads();
+            SimtState<D, HG> st;
+            st.start();
+            for (int tile = tile0; tile < tile1; ++tile) {
+                seen2 = fetch(tile + 2, page2);
+                page2 = page_of(tile + 3);
+                cp_wait<2>();
+                __syncwarp();
+                const uint8_t *k = smem + (warp * kStages + tile % kStages) * L::slot;
+                st.step(k, k + kWarpKeys * L::row, L::row, seen0, sQ, sP, lane);
+                seen0 = seen1;
+                seen1 = seen2;
+                __syncwarp();                           // the slot and sP are free again
             }
-            __syncwarp();
-            // ---- output channels DL lane .. of all 16 keys
-            const InT *vr = reinterpret_cast<const InT *>(slot + kWarpKeys * L::row) + DL * lane;
-#pragma unroll
-            for (int j = 0; j < kWarpKeys; j += 4) {
-                float x[4][DL];
-#pragma unroll
-                for (int jj = 0; jj < 4; ++jj) {
-                    const InT *p = reinterpret_cast<const InT *>(reinterpret_cast<const uint8_t *>(vr) + (j + jj) * L::row);
-#pragma unroll
-                    for (int y = 0; y < DL; ++y) x[jj][y] = to_f32(p[y]);
-                }
-#pragma unroll
-                for (int g = 0; g < HG; ++g) {
-                    const float4 p = la_load4(sP + g * kWarpKeys + j);
-#pragma unroll
-                    for (int y = 0; y < DL; ++y) {
-                        o[g][y] += p.x * x[0][y]; o[g][y] += p.y * x[1][y];
-                        o[g][y] += p.z * x[2][y]; o[g][y] += p.w * x[3][y];
-                    }
-                }
-            }
-            __syncwarp();                               // the slot and sP are free again
+            cp_wait<0>();
+            __syncthreads();
+            st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
         }
-        cp_wait<0>();
         // ---- the new token's key and value go to their place in the cache (one owner per head)
         if (new_at >= 0 && hb % blocks == 0 && new_at / kPagedTile >= tile0 && new_at / kPagedTile < tile1) {
-            const int page = a.block_table[(size_t)b * a.max_pages + new_at / a.page_size];
+            const unsigned int pi = quotient((unsigned int)new_at, by_page);
+            const int page = table[pi];
             if (page >= 0 && page < a.num_pages) {
-                const size_t dst = (((size_t)page * a.page_size + new_at % a.page_size) * a.Hkv + hk) * D;
+                const size_t dst = (((size_t)page * a.page_size + ((unsigned int)new_at - pi * by_page.d)) * a.Hkv + hk) * D;
                 const size_t src = ((size_t)b * a.Hkv + hk) * D;
                 for (int e = tid; e < CPR; e += kThreads) {
                     reinterpret_cast<uint4 *>(static_cast<InT *>(a.k_cache) + dst)[e] =
@@ -289,18 +488,6 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
             }
         }
         // ---- the four warps meet
-        __syncthreads();
-#pragma unroll
-        for (int g = 0; g < HG; ++g) {
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], x);
-            if (lane == 0) {
-                sML[(warp * HG + g) * 2] = m[g];
-                sML[(warp * HG + g) * 2 + 1] = l[g];
-            }
-#pragma unroll
-            for (int x = 0; x < DL; ++x) sO[(warp * HG + g) * D + DL * lane + x] = o[g][x];
-        }
         __syncthreads();
         float *slot = a.ws + ((size_t)blockIdx.x * 2 + (part > 0 ? 1 : 0)) * HG * (D + 2);
         for (int e = tid; e < nh * D; e += kThreads) {
@@ -321,6 +508,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 if (d == 0) { slot[HG * D + 2 * g] = top; slot[HG * D + 2 * g + 1] = sum; }
             }
         }
+        __syncthreads();                                // sO and sML lie where the next stretch's copies go
         u += (unsigned long long)(tile1 - tile0);
         ++part;
     }
@@ -384,7 +572,14 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
 template <int D, typename InT, int HG>
 constexpr int resident() { return 226 * 1024 / (PagedSmem<D, InT, HG>::total + 1024); }
 
-int heads_per_block(int group) { return group >= 8 ? 8 : group > 4 ? 8 : group > 2 ? 4 : group; }
+// Query heads that share one reading of the cache.  bf16: 8 columns of a product, or two
+// times 8 for larger groups (a third would no longer fit the registers); fp32: as many as the
+// group has, up to 8.
+int heads_per_block(int group, kda_dtype dtype)
+{
+    if (dtype == KDA_BF16) return group > 8 ? 16 : 8;
+    return group > 4 ? 8 : group > 2 ? 4 : group;
+}
 
 template <int D, typename InT, int HG>
 cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
@@ -394,6 +589,7 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
     static OncePerDevice once;
     cudaError_t e = set_shared_memory(kernel, L::total, once);
     if (e != cudaSuccess) return e;
+    static_assert(resident<D, InT, HG>() <= kMaxResident, "the workspace holds two stretches per CTA");
     const unsigned int grid = kSms * resident<D, InT, HG>();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -405,7 +601,7 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, divider((unsigned int)a.page_size))) != cudaSuccess) return e;
     note_launch();
     const int group = a.H / a.Hkv, blocks = (group + HG - 1) / HG;
     cfg.gridDim = dim3((unsigned)((size_t)a.B * a.Hkv * blocks));
@@ -415,14 +611,17 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
     return cudaGetLastError();
 }
 
-template <int D, typename InT>
+template <int D>
 cudaError_t launch_group(const PagedArgs &a, cudaStream_t stream)
 {
-    switch (heads_per_block(a.H / a.Hkv)) {
-    case 1: return launch_typed<D, InT, 1>(a, stream);
-    case 2: return launch_typed<D, InT, 2>(a, stream);
-    case 4: return launch_typed<D, InT, 4>(a, stream);
-    default: return launch_typed<D, InT, 8>(a, stream);
+    const int hg = heads_per_block(a.H / a.Hkv, a.dtype);
+    if (a.dtype == KDA_BF16)
+        return hg == 16 ? launch_typed<D, __nv_bfloat16, 16>(a, stream) : launch_typed<D, __nv_bfloat16, 8>(a, stream);
+    switch (hg) {
+    case 1: return launch_typed<D, float, 1>(a, stream);
+    case 2: return launch_typed<D, float, 2>(a, stream);
+    case 4: return launch_typed<D, float, 4>(a, stream);
+    default: return launch_typed<D, float, 8>(a, stream);
     }
 }
 
@@ -430,19 +629,12 @@ cudaError_t launch_group(const PagedArgs &a, cudaStream_t stream)
 
 size_t paged_workspace_bytes(int H, int Hkv, int D, kda_dtype dtype)
 {
-    (void)dtype;
-    // two stretches per CTA of a grid of at most 5 CTAs per SM
-    return sizeof(float) * (size_t)kSms * 5 * 2 * heads_per_block(H / Hkv) * (D + 2);
+    return sizeof(float) * (size_t)kSms * kMaxResident * 2 * heads_per_block(H / Hkv, dtype) * (D + 2);
 }
 
 cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t stream)
 {
-    if (a.D == 128) {
-        if (a.dtype == KDA_BF16) return launch_group<128, __nv_bfloat16>(a, stream);
-        return launch_group<128, float>(a, stream);
-    }
-    if (a.dtype == KDA_BF16) return launch_group<64, __nv_bfloat16>(a, stream);
-    return launch_group<64, float>(a, stream);
+    return a.D == 128 ? launch_group<128>(a, stream) : launch_group<64>(a, stream);
 }
 
 cudaError_t take_paged_device_status(unsigned int *status)
