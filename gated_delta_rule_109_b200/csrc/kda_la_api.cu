@@ -186,7 +186,7 @@ kda_status kda_paged_decode_step(const void *q, const void *k, const void *v, vo
     if (H % Hkv) return KDA_ERR_INVALID_ARG;
     if (dtype != KDA_BF16 && dtype != KDA_F32) return KDA_ERR_INVALID_ARG;
     if (!isfinite(scale)) return KDA_ERR_INVALID_ARG;
-    // the joining grid has one CTA per (row, key-value head, block of query heads)
+    // the joining grid has one CTA per row and query head
     if ((int64_t)B * H > (int64_t)INT32_MAX / 4) return KDA_ERR_INVALID_ARG;
     // a key's position and the tile behind the last one are 32-bit numbers
     if ((int64_t)max_pages * page_size > (int64_t)INT32_MAX - 1024) return KDA_ERR_INVALID_ARG;

@@ -1,7 +1,8 @@
 // Paged decode attention (the split of the work is in kda_paged.cuh).
 //
-// A CTA is four warps; of every unit of 64 keys a warp takes 16 and keeps its own running
-// maximum, sum and output, so that the warps meet only at the end of a stretch.  Each warp
+// A CTA is four warps; of every unit a warp takes 16 keys of one key-value head and keeps its
+// own running maximum, sum and output, so that the warps of a head meet only at the end of a
+// stretch.  Each warp
 // moves its keys and values through its own ring of shared-memory slots with 16-byte
 // asynchronous copies, kStages - 1 units ahead, and looks the page of its next unit up one
 // unit before that.  Reading the cache is what bounds it: every key and value is read once
@@ -26,7 +27,7 @@ __device__ unsigned int g_paged_status = 0;
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kWarpKeys = kPagedTile / kWarps, kStages = 3;
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kWarpKeys = 16, kStages = 3;
 constexpr int kSms = 148, kMaxResident = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -60,9 +61,13 @@ __device__ __forceinline__ int row_keys(const PagedArgs &a, int b)
     }
     return len + (a.k ? 1 : 0);
 }
-__device__ __forceinline__ int row_tiles(const PagedArgs &a, int b) { return (max(row_keys(a, b), 0) + kPagedTile - 1) / kPagedTile; }
+// Positions of a unit of HW heads, and units of a row for one group of heads and one block.
+template <int HW> constexpr int unit_keys() { return kWarps * kWarpKeys / HW; }
+template <int HW> __device__ __forceinline__ int tiles_of(int keys) { return (max(keys, 0) + unit_keys<HW>() - 1) / unit_keys<HW>(); }
 
-// CTAs of a grid that own units: each of them has at least one.
+// CTAs of a grid that own units: each of them has at least one.  (Two to six times as many
+// CTAs, for the hardware to even out, gained nothing and made more shares to join: 131071 keys
+// 108 -> 122 .. 230 us.)
 __device__ __forceinline__ unsigned long long owners_of(unsigned long long total, unsigned long long grid)
 {
     return total < grid ? total : grid;
@@ -71,16 +76,17 @@ __device__ __forceinline__ unsigned long long owners_of(unsigned long long total
 // Block-wide: the units of all rows, and row b with its first unit: the row asked for
 // (row >= 0), or else the one that the first unit of CTA `part` of `parts` belongs to (b = B
 // if there is none).  `per` units stand beside each other for every tile of a row (heads).
-struct RowAt { int b; unsigned long long first, total; };
+struct RowAt { int b, keys; unsigned long long first, total; };
+template <int HW>
 __device__ __forceinline__ RowAt find_row(const PagedArgs &a, unsigned long long per, unsigned long long part,
                                           unsigned long long parts, int row)
 {
     __shared__ unsigned long long s_sum[kThreads / 32], s_first;
-    __shared__ int s_b;
+    __shared__ int s_b, s_keys;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = (a.B + kThreads - 1) / kThreads, b0 = min(tid * n, a.B), b1 = min(b0 + n, a.B);
     unsigned long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += per * (unsigned long long)row_tiles(a, b);
+    for (int b = b0; b < b1; ++b) sum += per * (unsigned long long)tiles_of<HW>(row_keys(a, b));
     unsigned long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -99,13 +105,15 @@ __device__ __forceinline__ RowAt find_row(const PagedArgs &a, unsigned long long
     // by row (row >= 0), or by the first unit of part `part` of `parts`
     const unsigned long long at = total ? part * total / owners_of(total, parts) : 0;
     for (int b = b0; b < b1; ++b) {
-        const unsigned long long u = per * (unsigned long long)row_tiles(a, b);
-        if (row >= 0 ? b == row : (at >= before && at < before + u)) { s_b = b; s_first = before; }
+        const int keys = row_keys(a, b);
+        const unsigned long long u = per * (unsigned long long)tiles_of<HW>(keys);
+        if (row >= 0 ? b == row : (at >= before && at < before + u)) { s_b = b; s_keys = keys; s_first = before; }
         before += u;
     }
     __syncthreads();
     RowAt r;
     r.b = s_b;
+    r.keys = s_keys;
     r.first = s_first;
     r.total = total;
     return r;
@@ -141,8 +149,8 @@ struct PagedSmem {
     static constexpr int row = D * (int)sizeof(InT) + 16;                 // bytes; rows 4 banks apart
     static constexpr int slot = 2 * kWarpKeys * row;                      // K rows, then V rows
     static constexpr int ring = kWarps * kStages * slot;
-    static constexpr int off_q = ring;                                    // fp32: [HG][D], scaled by scale log2 e
-    static constexpr int off_p = off_q + (mma ? 0 : HG * D * 4);          // fp32: [warp][HG][16]
+    static constexpr int off_q = ring;                                    // fp32: [warp][HG][D], scaled by scale log2 e
+    static constexpr int off_p = off_q + (mma ? 0 : kWarps * HG * D * 4);          // fp32: [warp][HG][16]
     static constexpr int off_ml = off_p + (mma ? 0 : kWarps * HG * kWarpKeys * 4);    // [warp][HG] maximum, sum
     static constexpr int total = off_ml + kWarps * HG * 8;
     static_assert(kWarps * HG * D * 4 <= ring, "the warps' outputs meet in the ring");
@@ -348,7 +356,7 @@ struct SimtState {
     }
 };
 
-template <int D, typename InT, int HG>
+template <int D, typename InT, int HG, int HW>
 __global__ void __launch_bounds__(kThreads)
 paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
 {
@@ -356,6 +364,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
     constexpr int CPR = D * (int)sizeof(InT) / 16;      // 16-byte pieces of a row
     constexpr int RPI = 32 / CPR;                       // rows that a warp's copy instruction covers
     static_assert(CPR <= 32 && 32 % CPR == 0, "pieces");
+    constexpr int TW = kWarps / HW, kTile = unit_keys<HW>();     // warps of a head, positions of a unit
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + (uint32_t)(warp * kStages * L::slot);
@@ -366,24 +375,24 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     const int group = a.H / a.Hkv, blocks = (group + HG - 1) / HG;
-    const unsigned long long per = (unsigned long long)a.Hkv * blocks;
-    const RowAt at = find_row(a, per, blockIdx.x, gridDim.x, -1);
+    const unsigned long long per = (unsigned long long)(a.Hkv / HW) * blocks;
+    const RowAt at = find_row<HW>(a, per, blockIdx.x, gridDim.x, -1);
     const unsigned long long owners = owners_of(at.total, gridDim.x);
     if (blockIdx.x >= owners) return;
     unsigned long long u = (unsigned long long)blockIdx.x * at.total / owners;
     const unsigned long long u1 = ((unsigned long long)blockIdx.x + 1) * at.total / owners;
 
-    int b = at.b, part = 0;
+    int b = at.b, part = 0, n = at.keys, tiles = tiles_of<HW>(n);
     unsigned long long row_first = at.first;
     while (u < u1) {
-        int n = row_keys(a, b), tiles = (max(n, 0) + kPagedTile - 1) / kPagedTile;
         while (u >= row_first + per * tiles) {          // next row that has units
             row_first += per * tiles;
             n = row_keys(a, ++b);
-            tiles = (max(n, 0) + kPagedTile - 1) / kPagedTile;
+            tiles = tiles_of<HW>(n);
         }
-        const int hb = (int)((u - row_first) / tiles);          // (key-value head, block) of the stretch
-        const int hk = hb / blocks, h0 = hk * group + (hb % blocks) * HG, nh = min(HG, group - (hb % blocks) * HG);
+        const int hb = (int)((u - row_first) / tiles);          // (key-value heads, block) of the stretch
+        const int hk0 = hb / blocks * HW, blk0 = (hb % blocks) * HG, nh = min(HG, group - blk0);
+        const int hk = hk0 + warp / TW;                         // this warp's
         const int tile0 = (int)((u - row_first) % tiles);
         const int tile1 = (int)min((unsigned long long)tiles, (unsigned long long)tile0 + (u1 - u));
         const bool whole = tile0 == 0 && tile1 == tiles;
@@ -391,7 +400,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
         const int *table = a.block_table + (size_t)b * a.max_pages;
 
         // Page of this lane's key of a unit: key lane % 16 of the warp's 16 (-1: none).
-        auto key_of = [&](int tile) { return tile * kPagedTile + warp * kWarpKeys + (lane & 15); };
+        auto key_of = [&](int tile) { return tile * kTile + (warp % TW) * kWarpKeys + (lane & 15); };
         auto page_of = [&](int tile) {
             const int t = key_of(tile);
             return tile < tile1 && t < n ? table[quotient((unsigned int)t, by_page)] : -1;
@@ -432,7 +441,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
         static_assert(kStages == 3, "two units ahead");
         unsigned int seen0 = fetch(tile0, page_of(tile0)), seen1 = fetch(tile0 + 1, page_of(tile0 + 1)), seen2;
         int page2 = page_of(tile0 + 2);
-        const InT *qh = static_cast<const InT *>(a.q) + ((size_t)b * a.H + h0) * D;
+        const InT *qh = static_cast<const InT *>(a.q) + ((size_t)b * a.H + hk * group + blk0) * D;
         if constexpr (L::mma) {
             MmaState<D, HG> st;
             st.start(qh, nh, lane);
@@ -451,10 +460,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
             __syncthreads();
             st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
         } else {
-            float *sQ = reinterpret_cast<float *>(smem + L::off_q);
+            float *sQ = reinterpret_cast<float *>(smem + L::off_q) + warp * HG * D;
             float *sP = reinterpret_cast<float *>(smem + L::off_p) + warp * HG * kWarpKeys;
-            for (int e = tid; e < HG * D; e += kThreads) sQ[e] = e / D < nh ? to_f32(qh[e]) * (a.scale * kLog2e) : 0.f;
-            __syncthreads();
+            for (int e = lane; e < HG * D; e += 32) sQ[e] = e / D < nh ? to_f32(qh[e]) * (a.scale * kLog2e) : 0.f;
+            __syncwarp();
             SimtState<D, HG> st;
             st.start();
             for (int tile = tile0; tile < tile1; ++tile) {
@@ -472,14 +481,14 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
             __syncthreads();
             st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
         }
-        // ---- the new token's key and value go to their place in the cache (one owner per head)
-        if (new_at >= 0 && hb % blocks == 0 && new_at / kPagedTile >= tile0 && new_at / kPagedTile < tile1) {
+        // ---- the new token's keys and values go to their place in the cache (one owner per head)
+        if (new_at >= 0 && blk0 == 0 && new_at / kTile >= tile0 && new_at / kTile < tile1) {
             const unsigned int pi = quotient((unsigned int)new_at, by_page);
             const int page = table[pi];
             if (page >= 0 && page < a.num_pages) {
-                const size_t dst = (((size_t)page * a.page_size + ((unsigned int)new_at - pi * by_page.d)) * a.Hkv + hk) * D;
-                const size_t src = ((size_t)b * a.Hkv + hk) * D;
-                for (int e = tid; e < CPR; e += kThreads) {
+                const size_t dst = (((size_t)page * a.page_size + ((unsigned int)new_at - pi * by_page.d)) * a.Hkv + hk0) * D;
+                const size_t src = ((size_t)b * a.Hkv + hk0) * D;
+                for (int e = tid; e < HW * CPR; e += kThreads) {
                     reinterpret_cast<uint4 *>(static_cast<InT *>(a.k_cache) + dst)[e] =
                         reinterpret_cast<const uint4 *>(static_cast<const InT *>(a.k) + src)[e];
                     reinterpret_cast<uint4 *>(static_cast<InT *>(a.v_cache) + dst)[e] =
@@ -487,25 +496,28 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
                 }
             }
         }
-        // ---- the four warps meet
+        // ---- the warps of a head meet
         __syncthreads();
-        float *slot = a.ws + ((size_t)blockIdx.x * 2 + (part > 0 ? 1 : 0)) * HG * (D + 2);
-        for (int e = tid; e < nh * D; e += kThreads) {
-            const int g = e / D, d = e % D;
+        float *slot = a.ws + ((size_t)blockIdx.x * 2 + (part > 0 ? 1 : 0)) * HW * HG * (D + 2);
+        for (int e = tid; e < HW * nh * D; e += kThreads) {
+            const int hw = e / (nh * D), g = e / D % nh, d = e % D;
             float top = -INFINITY, sum = 0.f, acc = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sML[(w * HG + g) * 2]);
+            for (int w = 0; w < TW; ++w) top = fmaxf(top, sML[((hw * TW + w) * HG + g) * 2]);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float mw = sML[(w * HG + g) * 2], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
-                sum += f * sML[(w * HG + g) * 2 + 1];
-                acc += f * sO[(w * HG + g) * D + d];
+            for (int w = 0; w < TW; ++w) {
+                const int x = (hw * TW + w) * HG + g;
+                const float mw = sML[x * 2], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
+                sum += f * sML[x * 2 + 1];
+                acc += f * sO[x * D + d];
             }
             if (whole) {
-                static_cast<InT *>(a.out)[((size_t)b * a.H + h0 + g) * D + d] = la_round<InT>(sum > 0.f ? acc / sum : 0.f);
+                static_cast<InT *>(a.out)[((size_t)b * a.H + (hk0 + hw) * group + blk0 + g) * D + d] =
+                    la_round<InT>(sum > 0.f ? acc / sum : 0.f);
             } else {
-                slot[e] = acc;
-                if (d == 0) { slot[HG * D + 2 * g] = top; slot[HG * D + 2 * g + 1] = sum; }
+                float *mine = slot + hw * HG * (D + 2);
+                mine[g * D + d] = acc;
+                if (d == 0) { mine[HG * D + 2 * g] = top; mine[HG * D + 2 * g + 1] = sum; }
             }
         }
         __syncthreads();                                // sO and sML lie where the next stretch's copies go
@@ -514,28 +526,30 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
     }
 }
 
-// One CTA per (row, key-value head, block of query heads): rows without keys get zeros, and
-// stretches that several CTAs share are joined in the order of the keys.
-template <int D, typename InT, int HG>
+// One CTA per (row, query head): rows without keys get zeros, and stretches that several CTAs
+// share are joined, every fourth share by one warp, in the order of the keys.
+template <int D, typename InT, int HG, int HW>
 __global__ void __launch_bounds__(kThreads)
 paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
 {
+    constexpr int kShares = kSms * kMaxResident;        // owners there can be
+    __shared__ float s_acc[kWarps][D], s_sum[kWarps], s_top[kWarps], s_weight[kShares];
     const int group = a.H / a.Hkv, blocks = (group + HG - 1) / HG;
-    const unsigned long long per = (unsigned long long)a.Hkv * blocks;
-    const int b = blockIdx.x / (int)per, hb = blockIdx.x % (int)per;
+    const unsigned long long per = (unsigned long long)(a.Hkv / HW) * blocks;
+    const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = row_keys(a, b);
     if (n < 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int hk = hb / blocks, h0 = hk * group + (hb % blocks) * HG, nh = min(HG, group - (hb % blocks) * HG);
-    InT *out = static_cast<InT *>(a.out) + ((size_t)b * a.H + h0) * D;
+    InT *out = static_cast<InT *>(a.out) + (size_t)blockIdx.x * D;
     if (n == 0) {
-        for (int e = tid; e < nh * D; e += kThreads) out[e] = la_round<InT>(0.f);
+        if (tid < D) out[tid] = la_round<InT>(0.f);
         return;
     }
-    const RowAt at = find_row(a, per, 0, 1, b);
-    const unsigned long long tiles = (unsigned long long)(n + kPagedTile - 1) / kPagedTile;
+    const RowAt at = find_row<HW>(a, per, 0, 1, b);
+    const int hk = h / group, g = h % group % HG, hw = hk % HW, hb = hk / HW * blocks + h % group / HG;
+    const unsigned long long tiles = (unsigned long long)tiles_of<HW>(n);
     const unsigned long long x0 = at.first + hb * tiles, x1 = x0 + tiles - 1;
     // the CTA that has unit x: the largest c with c U / G <= x (G here: the owners)
     const unsigned long long owners = owners_of(at.total, grid);
@@ -544,27 +558,62 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
     // the first owner's stretch is its second part if it began with another one
     const unsigned int first_part = (unsigned long long)c0 * at.total / owners < x0 ? 1u : 0u;
     constexpr int DL = D / 32;
-    for (int g = warp; g < nh; g += kWarps) {
-        float top = -INFINITY;
-        for (unsigned int c = c0 + lane; c <= c1; c += 32) {
-            const float *slot = a.ws + ((size_t)c * 2 + (c == c0 ? first_part : 0u)) * HG * (D + 2);
-            top = fmaxf(top, slot[HG * D + 2 * g]);
+    auto share = [&](unsigned int c) {
+        return a.ws + (((size_t)c * 2 + (c == c0 ? first_part : 0u)) * HW + hw) * HG * (D + 2);
+    };
+    // the shares' weights 2^(m_c - m), and the sum
+    const int count = (int)(c1 - c0) + 1;
+    float top = -INFINITY, sum = 0.f;
+    for (int c = tid; c < count; c += kThreads) {
+        const float m = share(c0 + c)[HG * D + 2 * g];
+        s_weight[c] = m;
+        top = fmaxf(top, m);
+    }
+#pragma unroll
+    for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_top[w]);
+    for (int c = tid; c < count; c += kThreads) {
+        const float m = s_weight[c], f = m == -INFINITY ? 0.f : exp2f(m - top);
+        s_weight[c] = f;
+        sum += f * share(c0 + c)[HG * D + 2 * g + 1];
+    }
+#pragma unroll
+    for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    // eight shares at a time, so that their loads are under way together
+    float acc[DL];
+#pragma unroll
+    for (int y = 0; y < DL; ++y) acc[y] = 0.f;
+    for (int c = warp; c < count; c += 8 * kWarps) {
+        float x[8][DL];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float *slot = share(c0 + min(c + i * kWarps, count - 1)) + g * D + lane;
+#pragma unroll
+            for (int y = 0; y < DL; ++y) x[i][y] = slot[32 * y];
         }
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        float sum = 0.f, acc[DL];
+        for (int i = 0; i < 8; ++i) {
+            const float f = c + i * kWarps < count ? s_weight[c + i * kWarps] : 0.f;
 #pragma unroll
-        for (int x = 0; x < DL; ++x) acc[x] = 0.f;
-#pragma unroll 4
-        for (unsigned int c = c0; c <= c1; ++c) {
-            const float *slot = a.ws + ((size_t)c * 2 + (c == c0 ? first_part : 0u)) * HG * (D + 2);
-            const float mw = slot[HG * D + 2 * g], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
-            sum += f * slot[HG * D + 2 * g + 1];
-#pragma unroll
-            for (int x = 0; x < DL; ++x) acc[x] += f * slot[g * D + DL * lane + x];
+            for (int y = 0; y < DL; ++y) acc[y] += f * x[i][y];
         }
+    }
 #pragma unroll
-        for (int x = 0; x < DL; ++x) out[g * D + DL * lane + x] = la_round<InT>(sum > 0.f ? acc[x] / sum : 0.f);
+    for (int y = 0; y < DL; ++y) s_acc[warp][lane + 32 * y] = acc[y];
+    __syncthreads();
+    if (tid < D) {
+        float s = 0.f, o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            s += s_sum[w];
+            o += s_acc[w][tid];
+        }
+        out[tid] = la_round<InT>(s > 0.f ? o / s : 0.f);
     }
 }
 
@@ -581,11 +630,17 @@ int heads_per_block(int group, kda_dtype dtype)
     return group > 4 ? 8 : group > 2 ? 4 : group;
 }
 
-template <int D, typename InT, int HG>
+// Neighbouring key-value heads of a unit.
+// Two read 64 ragged rows (8 heads of 128 bf16) in 225 us, one in 228, four in 228; 128 rows of
+// 8 heads of 64: 215, 277, 221 us; 131071 keys of one row, where the shares of a head to be
+// joined grow with them: 101, 98, 108 us.
+int heads_per_unit(int Hkv) { return Hkv % 2 == 0 ? 2 : 1; }
+
+template <int D, typename InT, int HG, int HW>
 cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
 {
     using L = PagedSmem<D, InT, HG>;
-    auto kernel = paged_decode_kernel<D, InT, HG>;
+    auto kernel = paged_decode_kernel<D, InT, HG, HW>;
     static OncePerDevice once;
     cudaError_t e = set_shared_memory(kernel, L::total, once);
     if (e != cudaSuccess) return e;
@@ -603,12 +658,17 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, kernel, a, divider((unsigned int)a.page_size))) != cudaSuccess) return e;
     note_launch();
-    const int group = a.H / a.Hkv, blocks = (group + HG - 1) / HG;
-    cfg.gridDim = dim3((unsigned)((size_t)a.B * a.Hkv * blocks));
+    cfg.gridDim = dim3((unsigned)((size_t)a.B * a.H));
     cfg.dynamicSmemBytes = 0;
-    if ((e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, InT, HG>, a, grid)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, InT, HG, HW>, a, grid)) != cudaSuccess) return e;
     note_launch();
     return cudaGetLastError();
+}
+
+template <int D, typename InT, int HG>
+cudaError_t launch_heads(const PagedArgs &a, cudaStream_t stream)
+{
+    return heads_per_unit(a.Hkv) == 2 ? launch_typed<D, InT, HG, 2>(a, stream) : launch_typed<D, InT, HG, 1>(a, stream);
 }
 
 template <int D>
@@ -616,12 +676,12 @@ cudaError_t launch_group(const PagedArgs &a, cudaStream_t stream)
 {
     const int hg = heads_per_block(a.H / a.Hkv, a.dtype);
     if (a.dtype == KDA_BF16)
-        return hg == 16 ? launch_typed<D, __nv_bfloat16, 16>(a, stream) : launch_typed<D, __nv_bfloat16, 8>(a, stream);
+        return hg == 16 ? launch_heads<D, __nv_bfloat16, 16>(a, stream) : launch_heads<D, __nv_bfloat16, 8>(a, stream);
     switch (hg) {
-    case 1: return launch_typed<D, float, 1>(a, stream);
-    case 2: return launch_typed<D, float, 2>(a, stream);
-    case 4: return launch_typed<D, float, 4>(a, stream);
-    default: return launch_typed<D, float, 8>(a, stream);
+    case 1: return launch_heads<D, float, 1>(a, stream);
+    case 2: return launch_heads<D, float, 2>(a, stream);
+    case 4: return launch_heads<D, float, 4>(a, stream);
+    default: return launch_heads<D, float, 8>(a, stream);
     }
 }
 
@@ -629,7 +689,7 @@ cudaError_t launch_group(const PagedArgs &a, cudaStream_t stream)
 
 size_t paged_workspace_bytes(int H, int Hkv, int D, kda_dtype dtype)
 {
-    return sizeof(float) * (size_t)kSms * kMaxResident * 2 * heads_per_block(H / Hkv, dtype) * (D + 2);
+    return sizeof(float) * (size_t)kSms * kMaxResident * 2 * heads_per_unit(Hkv) * heads_per_block(H / Hkv, dtype) * (D + 2);
 }
 
 cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t stream)

@@ -6,21 +6,21 @@
 // the call carries them (they are written to the cache as well).  Query heads h of one
 // group h / (H / Hkv) share a key-value head.
 //
-// Split: a unit is kPagedTile consecutive keys of one (sequence, key-value head, block of
-// query heads), and all units lie on one line ordered by those three.  Of the U units CTA c of
-// G (at most U of them) takes [c U / G, (c + 1) U / G), whatever sequence they belong to, so
-// the CTAs' shares differ by at most one unit for every mix of lengths.  A stretch of units
-// with one owner is written out at once; one that several CTAs share leaves each owner's
-// running maximum, sum and unnormalised output in the workspace, and a second kernel joins
-// them.  The lengths are read on the device: nothing of the split depends on what the host
-// knows.
+// Split: a unit is 64 / HW consecutive keys of HW neighbouring key-value heads of one
+// sequence, for one block of their query heads, and all units lie on one line ordered by
+// sequence, heads, block and position.  HW is 2 where the number of key-value heads is even,
+// else 1: neighbouring heads are neighbours in memory, and a reader of two takes 512 B (bf16,
+// D = 128) of every position where a reader of one takes 256 B.  Of the U units CTA c of G (at
+// most U of them) takes [c U / G, (c + 1) U / G), whatever sequence they belong to, so the
+// CTAs' shares differ by at most one unit for every mix of lengths.  A stretch of units with
+// one owner is written out at once; one that several CTAs share leaves each owner's running
+// maximum, sum and unnormalised output in the workspace, and a second kernel joins them.
+// The lengths are read on the device: nothing of the split depends on what the host knows.
 #pragma once
 
 #include "kda_internal.cuh"
 
 namespace kda {
-
-constexpr int kPagedTile = 64;
 
 struct PagedArgs {
     const void *q, *k, *v;          // [B, H, D], [B, Hkv, D] or null, ditto
