@@ -39,31 +39,22 @@ struct LaArgs {
     const float *log_decay;     // [H] or null (lambda = 1)
     int B, T, H, dk, dv;
     kda_dtype dtype;
-    // Split of the sequence: nseg segments of seg_tokens (the last in time shorter); with
-    // more than one, `ws` holds [npass][B * H][nseg][dk][dv] fp32 states.
+    // Split of the sequence: nseg segments of seg_tokens (the last in time shorter), and the
+    // workspace that they need where there is more than one.
     int nseg, seg_tokens;
     float *ws;
 };
 
-// Tokens per chunk of the kernel that runs for this type and these head dimensions.
-int la_chunk(int dk, int dv, kda_dtype dtype);
 // Chooses a.nseg and a.seg_tokens (a.npass, sizes and dtype are set).
 void la_choose_segments(LaArgs &a);
-inline size_t la_workspace_bytes(const LaArgs &a)
-{
-    return a.nseg > 1 ? sizeof(float) * (size_t)a.npass * a.B * a.H * a.nseg * a.dk * a.dv : 0;
-}
-// All passes: with nseg > 1 every segment's own state, the scan over the segments, then
-// the outputs; else the outputs alone.
+size_t la_workspace_bytes(const LaArgs &a);
+// All passes of a.
 cudaError_t launch_la(const LaArgs &a, cudaStream_t stream);
 
-// fp32 arithmetic on CUDA cores: every supported type and head dimension.
-// states_only: each segment's state from zero goes to its slot of a.ws, no outputs.
-cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t stream);
-
-// Tensor cores (tcgen05): bf16 with dk = dv = 128.
+// Tensor cores (tcgen05): bf16 with dk = dv = 128.  One launch, segments included.
 bool la_tc_supported(int dk, int dv, kda_dtype dtype);
-cudaError_t launch_la_tc(const LaArgs &a, bool states_only, cudaStream_t stream);
+size_t la_tc_workspace_bytes(const LaArgs &a);
+cudaError_t launch_la_tc(const LaArgs &a, cudaStream_t stream);
 // Reads and clears the status word that the kernel sets when a bounded wait gives up.  Synchronous.
 cudaError_t take_la_device_status(unsigned int *status);
 

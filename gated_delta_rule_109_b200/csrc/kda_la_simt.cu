@@ -280,8 +280,8 @@ la_scan_kernel(const __grid_constant__ LaArgs a)
     }
 }
 
-}  // namespace
-
+// fp32 arithmetic on CUDA cores.  states_only: each segment's state from zero goes to its slot
+// of a.ws, [npass][B * H][nseg][dk][dv] fp32, no outputs.
 cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t stream)
 {
     if (a.dtype == KDA_BF16)
@@ -289,18 +289,19 @@ cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t strea
     return states_only ? launch_dims<float, true>(a, stream) : launch_dims<float, false>(a, stream);
 }
 
-int la_chunk(int dk, int dv, kda_dtype dtype) { return la_tc_supported(dk, dv, dtype) ? 128 : kC; }
+}  // namespace
 
-// Segments: with one per head the outputs' launch has npass B H CTAs that walk all chunks;
-// with n of them the walk is n times shorter, but every segment's state has to be known
-// first (a second walk over k and v) and joined.  The number with the least modelled time is
-// taken: waves of CTAs x chunks of a walk, the state walk at a fraction of the output walk's
-// cost per chunk, and a fixed cost (in chunks) for the two further launches.
+// Segments: with one per head a launch has npass B H CTAs that walk all chunks; with n of them
+// the walk is n times shorter, but every segment's own state has to be known first (a second
+// walk over k and v) and joined.  The number with the least modelled time is taken: waves of
+// CTAs x (chunks of a walk x the cost of both walks + a fixed cost of the join), in chunks of
+// the walk with outputs.
 void la_choose_segments(LaArgs &a)
 {
     constexpr int kSms = 148, kMaxSegments = 64;
-    constexpr double kStateCost = 0.5, kJoinCost = 2.0;
-    const int C = la_chunk(a.dk, a.dv, a.dtype);
+    const bool tc = la_tc_supported(a.dk, a.dv, a.dtype);
+    const int C = tc ? 128 : kC;
+    const double state_cost = tc ? 0.45 : 0.5, join_cost = tc ? 3.0 : 2.0, per_segment = tc ? 0.2 : 0.0;
     const int chunks = (a.T + C - 1) / C;
     const long long heads = (long long)a.npass * a.B * a.H;
     a.nseg = 1;
@@ -308,8 +309,8 @@ void la_choose_segments(LaArgs &a)
     double best = 0.0;
     for (int want = 1; want <= kMaxSegments && want <= chunks; ++want) {
         const int len = (chunks + want - 1) / want, n = (chunks + len - 1) / len;
-        const long long out_waves = (heads * n + kSms - 1) / kSms, state_waves = (heads * (n - 1) + kSms - 1) / kSms;
-        const double t = (double)out_waves * len + (n > 1 ? kStateCost * state_waves * len + kJoinCost : 0.0);
+        const long long waves = (heads * n + kSms - 1) / kSms;
+        const double t = (double)waves * (n > 1 ? len * (1.0 + state_cost) + join_cost + per_segment * n : len);
         if (want == 1 || t < best) {
             best = t;
             a.nseg = n;
@@ -318,18 +319,26 @@ void la_choose_segments(LaArgs &a)
     }
 }
 
+size_t la_workspace_bytes(const LaArgs &a)
+{
+    if (la_tc_supported(a.dk, a.dv, a.dtype)) return la_tc_workspace_bytes(a);
+    return a.nseg > 1 ? sizeof(float) * (size_t)a.npass * a.B * a.H * a.nseg * a.dk * a.dv : 0;
+}
+
+// CUDA cores with nseg > 1: every segment's own state, the scan over the segments, then the
+// outputs; else the outputs alone.
 cudaError_t launch_la(const LaArgs &a, cudaStream_t stream)
 {
-    const auto launch = la_tc_supported(a.dk, a.dv, a.dtype) ? launch_la_tc : launch_la_simt;
+    if (la_tc_supported(a.dk, a.dv, a.dtype)) return launch_la_tc(a, stream);
     if (a.nseg > 1) {
-        cudaError_t e = launch(a, true, stream);
+        cudaError_t e = launch_la_simt(a, true, stream);
         if (e != cudaSuccess) return e;
         const size_t n = (size_t)a.npass * a.B * a.H * (a.dk * a.dv / 4);
         la_scan_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         note_launch();
     }
-    return launch(a, false, stream);
+    return launch_la_simt(a, false, stream);
 }
 
 }  // namespace kda

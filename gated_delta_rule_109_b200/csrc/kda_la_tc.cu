@@ -1,11 +1,17 @@
 // Linear attention with one decay per head on the tensor cores (tcgen05): bf16 inputs,
 // dk = dv = 128 (the mathematics is in kda_la.cuh).
 //
-// One CTA walks the chunks of 128 tokens of one (pass, b, h, segment).  Per chunk, with
+// One CTA has one (pass, b, h, segment) and walks its chunks of 128 tokens.  Per chunk, with
 // accumulators in tensor memory:
 //     S = Q K^T                 P = f_intra lambda^|i-j| S on the causal side, as bf16, in place
 //     O = Q S0                  rescaled by rows with f_inter lambda^(i+1), then  O += P V
 //     U = K'^T V                K' = f_write lambda^(c-1-j) K;  S0 <- lambda^c S0 + U in registers
+// Where the heads alone do not fill the device the sequence is cut into segments.  A segment is
+// then walked twice: first over k and v alone for its own contribution to the state, which it
+// leaves in the workspace, then, with the contributions of all earlier segments added up to its
+// entering state, for the outputs.  Both walks are in one launch: a CTA waits (with a limit) for
+// the earlier segments' contributions.  CTAs take their work by a counter, earlier segments
+// first, so that whatever a CTA waits for has been taken by one that runs.
 // Roundings.  Q, K, V enter exactly.  P and the entering state S0 are rounded to bf16 for
 // their products: each output is a sum of such terms, so their errors together are of the
 // size of the output's own rounding to bf16.  The state that is carried is fp32: K' is
@@ -22,8 +28,7 @@
 // K'^T in tensor memory, the two groups of four by turns (ldmatrix transposes the K tile);
 // 12-19 carry the state (a thread is a key channel and half of the value columns); 20 moves
 // tiles by TMA; 21 issues Q K^T, Q S0 and P V, 22 the steps of U: a wait and an issue take a
-// warp about as long as the tensor core takes for a step, so one warp for all of them would
-// leave it idle half of the time (B4 H32 T16384: 452 us with one, LAT2 us with two).
+// warp about as long as the tensor core takes for a step.
 // Shared memory holds two stages of q, k, v (192 KB) and the state as an operand (32 KB); the
 // outputs of a chunk leave through its q tile.  Tiles are two boxes of 64 channels x 128
 // tokens in the 128-byte swizzle, which serves as K-major operand (channels contracted) and
@@ -58,24 +63,30 @@ constexpr uint32_t SM_WK = SM_WP + 256 * 4;           // [2][128] f_write lambda
 constexpr uint32_t SM_PW = SM_WK + 2 * 128 * 4;       // [129] lambda^n
 constexpr uint32_t SM_LC = SM_PW + 132 * 4;           // [2] lambda^c of a whole and of the ragged chunk, two floats each
 constexpr uint32_t SM_BAR = SM_LC + 16;
-constexpr int kKpSlots = 5, kKpSlotsStates = 10;       // slots of K', of the two kernels
+constexpr int kKpSlots = 5;
 enum Bar {
     FULL_Q = 0, FULL_K = 2, FULL_V = 4, FREE_K = 6, FREE_V = 8, OUT_READY = 10, U_READY = 12, U_FREE = 14,
-    KP_READY = 16, KP_FREE = KP_READY + kKpSlotsStates, S_READY = KP_FREE + kKpSlotsStates, QS_READY, PV_GO, PV_DONE,
+    KP_READY = 16, KP_FREE = KP_READY + kKpSlots, S_READY = KP_FREE + kKpSlots, QS_READY, PV_GO, PV_DONE,
     O_FREE, S0_READY, kBars
 };
-constexpr uint32_t SM_TMEM = SM_BAR + 8 * kBars;
+constexpr uint32_t SM_TMEM = SM_BAR + 8 * kBars;      // address of the tensor memory, work item
 constexpr uint32_t SM_TOTAL = SM_TMEM + 16;
 static_assert(SM_TOTAL <= 227 * 1024, "shared memory of a CTA");
 
-// Tensor memory columns.  Without outputs, S and O make room for five more slots of K' and a
-// second U, so that a chunk's U is computed while the one before is added to the state.
+// Tensor memory columns.  The walk without outputs has O's columns for a second U, so that a
+// chunk's U is computed while the one before is added to the state.
 constexpr uint32_t TM_S = 0, TM_P = 0, TM_O = 128, TM_U = 256, TM_KP = 384;
 constexpr uint32_t kKpPart = 8, kKpSlot = 3 * kKpPart;         // a slot: 16 tokens x 3 parts
-static_assert(TM_KP + kKpSlots * kKpSlot <= 512 && (kKpSlotsStates - kKpSlots) * kKpSlot <= TM_O, "slots");
-__device__ __forceinline__ uint32_t kp_column(int slot)
+static_assert(TM_KP + kKpSlots * kKpSlot <= 512, "slots");
+
+// The workspace: a counter of work items, for each contribution the number of warps that have
+// left their part, and [npass][B H][nseg] states of 64 KB in the order in which the state's
+// threads hold them: the contributions, and at nseg - 1 what segment 0 started from (it needs
+// that again for its outputs, when final_state, which may be initial_state, may be written).
+constexpr size_t kSlotFloats = (size_t)kD * kD;
+size_t flag_bytes(const LaArgs &a)
 {
-    return slot < kKpSlots ? TM_KP + kKpSlot * (uint32_t)slot : TM_S + kKpSlot * (uint32_t)(slot - kKpSlots);
+    return (sizeof(int) * (1 + (size_t)a.npass * a.B * a.H * a.nseg) + 255) & ~size_t(255);
 }
 
 struct LaMaps {
@@ -109,6 +120,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint
     asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%3, %4, %5, %6}], [%2];"
                  :: "r"(dst), "l"(tmap), "r"(mbar), "r"(c0), "r"(c1), "r"(c2), "r"(c3) : "memory");
+}
+
+// One head's 128 tokens from t on, both halves.
+__device__ __forceinline__ void load_tile(const void *tmap, uint32_t dst, uint32_t mbar, int h, int t, int b)
+{
+    mbar_expect_tx(mbar, 64 * 128 * 2 * 2);
+    tma_load_4d(dst, tmap, mbar, 0, h, t, b);
+    tma_load_4d(dst + 64 * 128 * 2, tmap, mbar, 64, h, t, b);
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
@@ -192,86 +211,196 @@ __device__ __forceinline__ void cut3(float2 x, uint32_t &hi, uint32_t &mid, uint
     lo = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x7632);
 }
 
-// What a CTA works on.
-struct Item { int seg, bh, ip; };
-__device__ __forceinline__ Item item_at(const LaArgs &a, bool states_only, unsigned int id)
+__device__ __forceinline__ int load_acquire(const int *p)
 {
-    const unsigned int nwork = states_only ? a.nseg - 1 : a.nseg, heads = a.B * a.H;
-    return {(int)(id % nwork), (int)((id / nwork) % heads), (int)(id / nwork / heads)};
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
-__device__ __forceinline__ float *state_slot(const LaArgs &a, const Item &x, int seg)
+__device__ __forceinline__ float4 load_l2(const float4 *p)
 {
-    return a.ws + (((size_t)x.ip * a.B * a.H + x.bh) * a.nseg + seg) * kD * kD;
+    float4 v;
+    asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    return v;
 }
 
-// STATES_ONLY: the segment's own state from zero goes to slot seg + 1 of the workspace; no
-// outputs (warps 0-3 idle, no q).
-template <bool STATES_ONLY>
+// ---- the state of work item x, 64 floats a thread: key channel r, value columns 64 part ..
+__device__ __forceinline__ int reread(uint32_t saddr)
+{
+    int v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(saddr) : "memory");
+    return v;
+}
+__device__ __forceinline__ const LaPass &pass_of(const LaArgs &a, int x, int &bh)
+{
+    const int heads = a.B * a.H;
+    bh = x % heads;
+    return a.pass[x / heads % a.npass];
+}
+// The pass's initial state, or zeros (`zero`, or none given).  32 rows x 32 columns at a time go
+// through 4 KB of shared memory of the warp's own, so that global memory is read by whole
+// sectors and a thread still gets its row; one way for all cases, so that S has one definition.
+__device__ __forceinline__ void load_initial(const LaArgs &a, int x, bool zero, int quad, int part, int lane, uint32_t buf,
+                                             float (&S)[64])
+{
+    int bh;
+    const LaPass &ps = pass_of(a, x, bh);
+    const float *s0 = ps.s0 && !zero ? ps.s0 + (size_t)bh * kSlotFloats : nullptr;
+    const uint32_t mine = buf + (uint32_t)lane * 128u, swz = (uint32_t)(lane & 7) << 4;
+#pragma unroll
+    for (int c0 = 0; c0 < 64; c0 += 32) {
+        __syncwarp();
+#pragma unroll 2
+        for (int i = 0; i < 8; ++i) {
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+            uint32_t dst;
+            if (s0 && ps.s0_transposed) {                   // lane = row, four columns of it
+                const float *p = s0 + (64 * part + c0 + 4 * i) * kD + 32 * quad + lane;
+                u = make_float4(p[0], p[kD], p[2 * kD], p[3 * kD]);
+                dst = mine + ((16u * (uint32_t)i) ^ swz);
+            } else {                                        // eight lanes = 128 bytes of a row
+                const int row = 4 * i + (lane >> 3), piece = lane & 7;
+                if (s0) u = *reinterpret_cast<const float4 *>(s0 + (32 * quad + row) * kD + 64 * part + c0 + 4 * piece);
+                dst = buf + (uint32_t)(row * 128) + ((16u * (uint32_t)piece) ^ ((uint32_t)(row & 7) << 4));
+            }
+            st_shared16(dst, __float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z), __float_as_uint(u.w));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t src = mine + ((16u * (uint32_t)i) ^ swz);
+            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(S[c0 + 4 * i]), "=f"(S[c0 + 4 * i + 1]), "=f"(S[c0 + 4 * i + 2]), "=f"(S[c0 + 4 * i + 3])
+                         : "r"(src) : "memory");
+        }
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void store_final(const LaArgs &a, int x, int r, int part, const float (&S)[64])
+{
+    int bh;
+    const LaPass &ps = pass_of(a, x, bh);
+    if (!ps.sT || x / (a.B * a.H) / a.npass != a.nseg - 1) return;
+    float *dst = ps.sT + (size_t)bh * kSlotFloats + r * kD + 64 * part;
+#pragma unroll
+    for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+}
+// S to state `g` of the workspace's chain of item x: 16 x float4 of thread `me`, a warp's 512
+// bytes beside each other; `tell`: counted for those that wait for it.
+__device__ __forceinline__ void leave_state(const LaArgs &a, int x, int g, int me, bool tell, int *flags, float *slots,
+                                            const float (&S)[64])
+{
+    const size_t at = (size_t)(x % (a.npass * a.B * a.H)) * a.nseg + g;
+    float4 *dst = reinterpret_cast<float4 *>(slots + at * kSlotFloats) + me;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dst[256 * i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+    if (tell) {
+        __threadfence();
+        __syncwarp();
+        if ((me & 31) == 0) atomicAdd(flags + 1 + at, 1);
+    }
+}
+// The state that enters the segment, whatever S held: the contributions of all segments before
+// it, or what segment 0 started from.  False if one did not come.
+__device__ __forceinline__ bool entering_state(const LaArgs &a, int x, int me, const int *flags, const float *slots,
+                                               float (&S)[64])
+{
+    const int heads = a.npass * a.B * a.H, seg = x / heads;
+    const size_t chain = (size_t)(x % heads) * a.nseg;
+    int bh;
+    const LaPass &ps = pass_of(a, x, bh);
+    for (int g = 0; g < max(seg, 1); ++g) {
+        const size_t at = chain + (seg == 0 ? a.nseg - 1 : g);
+        const long long t0 = clock64();
+        while (seg > 0 && !__all_sync(0xffffffffu, load_acquire(flags + 1 + at) == kStateWarps))
+            if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) {
+                atomicOr(&g_la_device_status, 1u);
+                return false;
+            }
+        int t0g, t1g;
+        la_segment(g, a.nseg, a.seg_tokens, a.T, ps.rev, t0g, t1g);
+        const double l = g == 0 ? 0.0 : la_power(a.log_decay, bh % a.H, t1g - t0g);
+        const float lh = (float)l, ll = (float)(l - (double)lh);
+        const float4 *src = reinterpret_cast<const float4 *>(slots + at * kSlotFloats) + me;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float4 w = load_l2(src + 256 * i);
+            S[4 * i] = fmaf(lh, S[4 * i], fmaf(ll, S[4 * i], w.x));
+            S[4 * i + 1] = fmaf(lh, S[4 * i + 1], fmaf(ll, S[4 * i + 1], w.y));
+            S[4 * i + 2] = fmaf(lh, S[4 * i + 2], fmaf(ll, S[4 * i + 2], w.z));
+            S[4 * i + 3] = fmaf(lh, S[4 * i + 3], fmaf(ll, S[4 * i + 3], w.w));
+        }
+    }
+    return true;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps maps)
+la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps maps, int *flags, float *slots)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = (uint32_t)__cvta_generic_to_shared(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Item item = item_at(a, STATES_ONLY, blockIdx.x);
-    const int seg = item.seg, bh = item.bh, ip = item.ip;
-    const LaPass &ps = a.pass[ip];
-    const int b = bh / a.H, h = bh % a.H, rev = ps.rev;
-    int t_lo, t_hi;
-    la_segment(seg, a.nseg, a.seg_tokens, a.T, rev, t_lo, t_hi);
-    const int n0 = t_lo / kC, nchunks = (t_hi + kC - 1) / kC - n0;
-    const int c_last = t_hi - (n0 + nchunks - 1) * kC;          // tokens of the chunk at the segment's end in time
-    auto chunk_at = [&](int it) { return n0 + (rev ? nchunks - 1 - it : it); };
+    const int heads = a.npass * a.B * a.H;
     auto bar = [&](int i) { return sb + SM_BAR + 8u * (uint32_t)i; };
-    // steps of the walk from three_at on keep all three parts of K'
-    int three_at = 0;
-    if (a.log_decay) {
-        const float fade = 6.f / (-1.4426950408889634f * a.log_decay[h]);       // tokens to 2^-6 (inf: never)
-        three_at = fade >= 0.f && fade < (float)(nchunks * kC) ? max(0, nchunks - 1 - (int)(fade / kC) - 1) : 0;
-    }
-    if (!STATES_ONLY && (seg != a.nseg - 1 || !ps.sT)) three_at = nchunks;
-    const int tail_at = c_last == kC ? -1 : rev ? 0 : nchunks - 1;      // the walk's step that is the ragged chunk
 
-    // ---- set up: barriers, tensor memory, powers of lambda
-    float *sWP = reinterpret_cast<float *>(smem + SM_WP), *sWK = reinterpret_cast<float *>(smem + SM_WK);
-    float *sPW = reinterpret_cast<float *>(smem + SM_PW);
-    if (tid == 0) {
+    // ---- barriers, tensor memory, the work item
+    if (warp == kTmaWarp && lane == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const int count = (i >= FREE_K && i < FREE_V) ? (STATES_ONLY ? kKeyWarps : kKeyWarps + 1)
-                              : (i >= FREE_V && i < OUT_READY) ? (STATES_ONLY ? 1 : 2)
+            const int count = (i >= FREE_K && i < FREE_V) ? kKeyWarps + 1
+                              : (i >= FREE_V && i < OUT_READY) ? 2
                               : (i >= OUT_READY && i < U_READY) || i == PV_GO || i == O_FREE ? kRowWarps
                               : (i >= KP_READY && i < KP_FREE) ? kKeyWarps / 2
                               : (i >= U_FREE && i < KP_READY) || i == S0_READY ? kStateWarps : 1;
             mbar_init(bar(i), (uint32_t)count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *reinterpret_cast<int *>(smem + SM_TMEM + 4) = a.nseg > 1 ? atomicAdd(flags, 1) : (int)blockIdx.x;
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(sb + SM_TMEM) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    if (tid <= kC) {
-        const float p = (float)la_power(a.log_decay, h, tid);
-        sPW[tid] = p;
-        if (tid < kC) {
-            const int up = 127 + tid, down = 127 - tid;         // i - j = tid, and -tid
-            sWP[up] = (!rev || tid == 0) ? p * ps.f_intra : 0.f;
-            if (tid > 0) sWP[down] = rev ? p * ps.f_intra : 0.f;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (tid >= 2 * kC && tid < 2 * kC + 2) {
-        const double l = la_power(a.log_decay, h, tid == 2 * kC ? kC : c_last);
-        reinterpret_cast<float2 *>(smem + SM_LC)[tid - 2 * kC] = make_float2((float)l, (float)(l - (double)(float)l));
-    }
-    if (tid < 2 * kC) {
+    const int item = *reinterpret_cast<const int *>(smem + SM_TMEM + 4);
+    const int seg = item / heads, ip = item % heads / (a.B * a.H), bh = item % (a.B * a.H);
+    const LaPass &ps = a.pass[ip];
+    const int b = bh / a.H, h = bh % a.H, rev = ps.rev;
+    int t_lo, t_hi;
+    la_segment(seg, a.nseg, a.seg_tokens, a.T, rev, t_lo, t_hi);
+    const int n0 = t_lo / kC, nchunks = (t_hi + kC - 1) / kC - n0;
+    const int c_last = t_hi - (n0 + nchunks - 1) * kC;          // tokens of the chunk at the segment's end in time
+    const int tail_at = c_last == kC ? -1 : rev ? 0 : nchunks - 1;      // the walk's step that is the ragged chunk
+    // steps 0 .. nown - 1: the segment's own contribution; nown .. nown + nchunks - 1: the outputs
+    const int nown = seg < a.nseg - 1 ? nchunks : 0, nsteps = nown + nchunks;
+    auto chunk_at = [&](int j) { return n0 + (rev ? nchunks - 1 - j : j); };
+
+    if (warp == kTmaWarp) {
+        // the first tiles are on their way while the others set up
+        if (lane == 0)
+            for (int it = 0; it < 2 && it < nsteps; ++it) {
+                const int t = chunk_at(it < nown ? it : it - nown) * kC;
+                load_tile(&maps.k[ip], sb + SM_K + it * kTile, bar(FULL_K + it), h, t, b);
+                load_tile(&maps.v[ip], sb + SM_V + it * kTile, bar(FULL_V + it), h, t, b);
+                if (it >= nown) load_tile(&maps.q[ip], sb + SM_Q + (it - nown) * kTile, bar(FULL_Q + it - nown), h, t, b);
+            }
+        __syncwarp();
+    } else if (tid < 256) {
+        // powers of lambda in 64 bits
+        float *sWP = reinterpret_cast<float *>(smem + SM_WP), *sWK = reinterpret_cast<float *>(smem + SM_WK);
         const int j = tid & (kC - 1), c = tid < kC ? kC : c_last;
-        sWK[tid] = ps.f_write * sPW[rev ? j + 1 : max(c - 1 - j, 0)];
+        sWK[tid] = ps.f_write * (float)la_power(a.log_decay, h, rev ? j + 1 : max(c - 1 - j, 0));
+        const int apart = tid - 127;                            // i - j
+        sWP[tid] = (rev ? apart <= 0 : apart >= 0) ? ps.f_intra * (float)la_power(a.log_decay, h, abs(apart)) : 0.f;
+    } else if (tid < 256 + kC + 1) {
+        reinterpret_cast<float *>(smem + SM_PW)[tid - 256] = (float)la_power(a.log_decay, h, tid - 256);
+    } else if (tid < 256 + kC + 3) {
+        const int ragged = tid - (256 + kC + 1);
+        const double l = la_power(a.log_decay, h, ragged ? c_last : kC);
+        reinterpret_cast<float2 *>(smem + SM_LC)[ragged] = make_float2((float)l, (float)(l - (double)(float)l));
     }
     __syncthreads();
-    constexpr int kSlots = STATES_ONLY ? kKpSlotsStates : kKpSlots;
     constexpr uint32_t tm = 0;              // all 512 columns: they begin at 0
     constexpr uint32_t id_nt = idesc_bf16(128, 128, 0, 0), id_nn = idesc_bf16(128, 128, 0, 1);
 
@@ -290,73 +419,82 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(i));
     };
+    // Steps of a walk whose K' has all three parts: from this one on.  `tokens` come behind
+    // the segment; counted one chunk short, so that a ragged chunk leaves no step out.
+    auto three_from = [&](bool wanted) {
+        if (!wanted) return nchunks;
+        if (!a.log_decay) return 0;
+        const float fade = 6.f / (-1.4426950408889634f * a.log_decay[h]);       // tokens to 2^-6
+        if (!(fade >= 0.f && fade < 1e9f)) return 0;                            // it does not fade
+        const float behind = rev ? (float)t_lo : (float)(a.T - t_hi);
+        return min(max(nchunks - 2 - (int)floorf((fade - behind) * (1.f / kC)), 0), nchunks);
+    };
 
     if (warp < kRowWarps) {
-        if (!STATES_ONLY) {
-            const int i = 32 * warp + lane;
-            const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
-            for (int it = 0; it < nchunks; ++it) {
-                const int c = it == tail_at ? c_last : kC, st = it & 1;
-                // ---- P from S
-                if (!wait_warp(S_READY, it)) break;
-                tc_fence_after();
+        const float *sWP = reinterpret_cast<const float *>(smem + SM_WP), *sPW = reinterpret_cast<const float *>(smem + SM_PW);
+        const int i = 32 * warp + lane;
+        const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
+        for (int j = 0; j < nchunks; ++j) {
+            const int c = j == tail_at ? c_last : kC, st = j & 1;
+            // ---- P from S
+            if (!wait_warp(S_READY, j)) break;
+            tc_fence_after();
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb) {
-                    uint32_t p[16];
-                    if (rev ? cb >= warp : cb <= warp) {
-                        float s[32];
-                        tmem_ld32(row + TM_S + 32 * cb, s);
-                        const float *w = sWP + 127 + i - 32 * cb;
+            for (int cb = 0; cb < 4; ++cb) {
+                uint32_t p[16];
+                if (rev ? cb >= warp : cb <= warp) {
+                    float s[32];
+                    tmem_ld32(row + TM_S + 32 * cb, s);
+                    const float *w = sWP + 127 + i - 32 * cb;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) p[j] = pack_bf16(s[2 * j] * w[-2 * j], s[2 * j + 1] * w[-2 * j - 1]);
-                    } else {
+                    for (int x = 0; x < 16; ++x) p[x] = pack_bf16(s[2 * x] * w[-2 * x], s[2 * x + 1] * w[-2 * x - 1]);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) p[j] = 0u;
-                    }
-                    tmem_st16u(row + TM_P + 16 * cb, p);
+                    for (int x = 0; x < 16; ++x) p[x] = 0u;
                 }
-                // ---- O <- f_inter lambda^(.) O
-                if (!wait_warp(QS_READY, it)) break;
-                tc_fence_after();
-                const float f = ps.f_inter * sPW[rev ? max(c - 1 - i, 0) : i + 1];
+                tmem_st16u(row + TM_P + 16 * cb, p);
+            }
+            // ---- O <- f_inter lambda^(.) O
+            if (!wait_warp(QS_READY, j)) break;
+            tc_fence_after();
+            const float f = ps.f_inter * sPW[rev ? max(c - 1 - i, 0) : i + 1];
 #pragma unroll
-                for (int cb = 0; cb < 8; ++cb) {
-                    float o[16];
-                    tmem_ld16(row + TM_O + 16 * cb, o);
+            for (int cb = 0; cb < 8; ++cb) {
+                float o[16];
+                tmem_ld16(row + TM_O + 16 * cb, o);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) o[j] *= f;
-                    tmem_st16(row + TM_O + 16 * cb, o);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive_warp(PV_GO);
-                // ---- outputs through the q tile
-                if (!wait_warp(PV_DONE, it)) break;
-                tc_fence_after();
-                const uint32_t dst = sb + SM_Q + (uint32_t)(st * kTile + i * 128);
+                for (int x = 0; x < 16; ++x) o[x] *= f;
+                tmem_st16(row + TM_O + 16 * cb, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(PV_GO);
+            // ---- outputs through the q tile
+            if (!wait_warp(PV_DONE, j)) break;
+            tc_fence_after();
+            const uint32_t dst = sb + SM_Q + (uint32_t)(st * kTile + i * 128);
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb) {
-                    float o[32];
-                    tmem_ld32(row + TM_O + 32 * cb, o);
+            for (int cb = 0; cb < 4; ++cb) {
+                float o[32];
+                tmem_ld32(row + TM_O + 32 * cb, o);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        st_shared16(dst + (cb >> 1) * kHalf + (uint32_t)(((4 * (cb & 1) + x) ^ (i & 7)) << 4),
-                                    pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
-                                    pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
-                }
-                tc_fence_before();
-                proxy_fence();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(O_FREE));
-                    mbar_arrive(bar(OUT_READY + st));
-                }
+                for (int x = 0; x < 4; ++x)
+                    st_shared16(dst + (cb >> 1) * kHalf + (uint32_t)(((4 * (cb & 1) + x) ^ (i & 7)) << 4),
+                                pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
+                                pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
+            }
+            tc_fence_before();
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(O_FREE));
+                mbar_arrive(bar(OUT_READY + st));
             }
         }
     } else if (warp < kStateWarp0) {
         // ---- K'^T: slots of 16 tokens, this group's every second one; 32 key channels a warp
         const int quad = warp & 3, group = (warp - kRowWarps) >> 2;
-        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16);
+        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_KP;
         int slot = group, use = 0;                              // of the ring: every second one
         reg_dec<kKeyRegs>();
         // ldmatrix: lanes 8 m .. 8 m + 7 name the rows (tokens) of matrix m: tokens 8 (m / 2) ..,
@@ -364,9 +502,12 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         const int jr = lane & 7, m = lane >> 3, piece = 4 * (quad & 1) + (m & 1);
         const uint32_t kt = sb + SM_K + (quad >> 1) * kHalf + (uint32_t)((16 * group + 8 * (m >> 1) + jr) * 128);
         const uint32_t off0 = (uint32_t)((piece ^ jr) << 4), off1 = (uint32_t)(((piece + 2) ^ jr) << 4);
-        for (int it = 0; it < nchunks; ++it) {
-            const int st = it & 1;
-            const float *wk = sWK + (it == tail_at ? kC : 0) + 16 * group + 2 * (lane & 3);
+        const float *sWK = reinterpret_cast<const float *>(smem + SM_WK) + 16 * group + 2 * (lane & 3);
+        const int three_own = three_from(ps.sT), three_out = nown + three_from(ps.sT && seg == a.nseg - 1);
+        for (int it = 0; it < nsteps; ++it) {
+            const int st = it & 1, j = it < nown ? it : it - nown;
+            const float *wk = sWK + (j == tail_at ? kC : 0);
+            const bool three = it >= (it < nown ? three_own : three_out);
             if (!wait_warp(FULL_K + st, it >> 1)) break;
 #pragma unroll 1
             for (int s4 = 0; s4 < 4; ++s4) {
@@ -376,7 +517,6 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 uint32_t k0[4], k1[4], hi[8], mid[8], lo[8];
                 ldmatrix4_trans(src + off0, k0);
                 ldmatrix4_trans(src + off1, k1);
-                const bool three = it >= three_at;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float2 x = scale_pair(e < 4 ? k0[e & 3] : k1[e & 3], (e & 2) ? w1 : w0);
@@ -387,7 +527,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 tc_fence_after();
 #pragma unroll
                 for (int e = 0; e < 8; e += 4) {
-                    const uint32_t dst = row + ((uint32_t)(4 * e) << 16) + kp_column(slot);
+                    const uint32_t dst = row + ((uint32_t)(4 * e) << 16) + slot * kKpSlot;
                     tmem_st_16x8(dst, hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
                     tmem_st_16x8(dst + kKpPart, mid[e], mid[e + 1], mid[e + 2], mid[e + 3]);
                     if (three) tmem_st_16x8(dst + 2 * kKpPart, lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
@@ -396,35 +536,39 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 tc_fence_before();
                 arrive_warp(KP_READY + slot);
                 slot += 2;
-                if (slot >= kSlots) { slot -= kSlots; ++use; }
+                if (slot >= kKpSlots) { slot -= kKpSlots; ++use; }
             }
             if (!ok) break;
             arrive_warp(FREE_K + st);
         }
     } else if (warp < kTmaWarp) {
-        // ---- the state: key channel r, value columns 64 part ..
+        // ---- the state: key channel r, value columns 64 part ..  (The walk leaves no registers for
+        // what is needed before and after it: that is read from the work item again.)
         const int quad = warp & 3, part = (warp - kStateWarp0) >> 2;
         const int r = 32 * quad + lane;
         const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + 64 * part;
         reg_inc<kStateRegs>();
         float S[64];
-        {
-            const float *s0 = STATES_ONLY ? nullptr : a.nseg > 1 ? state_slot(a, item, seg)
-                              : ps.s0 ? ps.s0 + (size_t)bh * kD * kD : nullptr;
-            if (!s0) {
+        // segment 0's own contribution includes the initial state
+        const uint32_t buf = sb + SM_S0 + (uint32_t)(4096 * (4 * part + quad));     // until the state is published
+        load_initial(a, reread(sb + SM_TMEM + 4), seg != 0, quad, part, lane, buf, S);
+        // S <- lambda^c S + U
+        auto absorb = [&](int ub, int use, int j) {
+            if (!wait_warp(U_READY + ub, use)) return false;
+            tc_fence_after();
+            const float2 l = reinterpret_cast<const float2 *>(smem + SM_LC)[j == tail_at];
+            const uint32_t src = row + (ub ? TM_O : TM_U);
 #pragma unroll
-                for (int x = 0; x < 64; ++x) S[x] = 0.f;
-            } else if (a.nseg == 1 && ps.s0_transposed) {
+            for (int x = 0; x < 64; x += 8) {
+                float u[8];
+                tmem_ld8(src + x, u);
 #pragma unroll
-                for (int x = 0; x < 64; ++x) S[x] = s0[(64 * part + x) * kD + r];
-            } else {
-#pragma unroll
-                for (int x = 0; x < 64; x += 4) {
-                    const float4 u = *reinterpret_cast<const float4 *>(s0 + r * kD + 64 * part + x);
-                    S[x] = u.x; S[x + 1] = u.y; S[x + 2] = u.z; S[x + 3] = u.w;
-                }
+                for (int y = 0; y < 8; ++y) S[x + y] = fmaf(l.x, S[x + y], fmaf(l.y, S[x + y], u[y]));
             }
-        }
+            tc_fence_before();
+            arrive_warp(U_FREE + ub);
+            return true;
+        };
         const uint32_t s0_row = sb + SM_S0 + part * kHalf + (uint32_t)(r * 128), s0_swz = (uint32_t)(r & 7) << 4;
         auto publish = [&] {                                    // the state as the operand of Q S0
 #pragma unroll
@@ -435,135 +579,121 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
             proxy_fence();
             arrive_warp(S0_READY);
         };
-        if (!STATES_ONLY) publish();
-        for (int it = 0; it < nchunks; ++it) {
-            // S <- lambda^c S + U
-            const int ub = STATES_ONLY ? it & 1 : 0;
-            if (!wait_warp(U_READY + ub, STATES_ONLY ? it >> 1 : it)) break;
-            tc_fence_after();
-            const float2 l = reinterpret_cast<const float2 *>(smem + SM_LC)[it == tail_at];
-#pragma unroll
-            for (int x = 0; x < 64; x += 8) {
-                float u[8];
-                tmem_ld8(row + (ub ? TM_O : TM_U) + x, u);
-#pragma unroll
-                for (int y = 0; y < 8; ++y) S[x + y] = fmaf(l.x, S[x + y], fmaf(l.y, S[x + y], u[y]));
+        if (a.nseg > 1) {
+            const int me = tid - 32 * kStateWarp0;
+            if (seg == 0) leave_state(a, reread(sb + SM_TMEM + 4), a.nseg - 1, me, false, flags, slots, S);
+            for (int j = 0; j < nown; ++j)
+                if (!absorb(j & 1, j >> 1, j)) break;
+            if (ok) {
+                const int x0 = reread(sb + SM_TMEM + 4);
+                if (nown > 0) leave_state(a, x0, x0 / heads, me, true, flags, slots, S);
+                ok = entering_state(a, x0, me, flags, slots, S);
             }
-            tc_fence_before();
-            arrive_warp(U_FREE + ub);
-            if (!STATES_ONLY && it + 1 < nchunks) {
-                if (!wait_warp(QS_READY, it)) break;            // the operand of this chunk has been read
+        }
+        if (ok) publish();
+        for (int j = 0; j < nchunks && ok; ++j) {
+            if (!absorb(0, ((nown + 1) >> 1) + j, j)) break;
+            if (j + 1 < nchunks) {
+                if (!wait_warp(QS_READY, j)) break;             // the operand of this chunk has been read
                 publish();
             }
         }
-        unsigned int id;                        // read again: the loop has no register for what follows from it
-        asm volatile("mov.u32 %0, %%ctaid.x;" : "=r"(id));
-        const Item end = item_at(a, STATES_ONLY, id);
-        float *dst = STATES_ONLY ? state_slot(a, end, end.seg + 1)
-                     : (end.seg == a.nseg - 1 && a.pass[end.ip].sT) ? a.pass[end.ip].sT + (size_t)end.bh * kD * kD : nullptr;
-        if (dst && ok)
-#pragma unroll
-            for (int x = 0; x < 64; x += 4)
-                *reinterpret_cast<float4 *>(dst + r * kD + 64 * part + x) = make_float4(S[x], S[x + 1], S[x + 2], S[x + 3]);
+        if (ok) store_final(a, reread(sb + SM_TMEM + 4), r, part, S);
     } else if (warp == kTmaWarp) {
         if (lane == 0) {
-            auto load = [&](const CUtensorMap *m, uint32_t dst, int full, int n) {
-                mbar_expect_tx(bar(full), kTile);
-                tma_load_4d(dst, m, bar(full), 0, h, n * kC, b);
-                tma_load_4d(dst + kHalf, m, bar(full), 64, h, n * kC, b);
+            auto store = [&](int j) {
+                const uint32_t src = sb + SM_Q + (j & 1) * kTile;
+                const int t = chunk_at(j) * kC;
+                tma_store_4d(&maps.out[ip], src, 0, h, t, b);
+                tma_store_4d(&maps.out[ip], src + kHalf, 64, h, t, b);
+                bulk_commit();
             };
-            int issued = 0;
-            for (int it = 0; it < nchunks; ++it) {
-                const int n = chunk_at(it), st = it & 1;
-                if (it >= 2 && !wait(FREE_K + st, (it >> 1) - 1)) break;
-                load(&maps.k[ip], sb + SM_K + st * kTile, FULL_K + st, n);
-                if (!STATES_ONLY && it < 2) load(&maps.q[ip], sb + SM_Q + st * kTile, FULL_Q + st, n);
-                if (it >= 2 && !wait(FREE_V + st, (it >> 1) - 1)) break;
-                load(&maps.v[ip], sb + SM_V + st * kTile, FULL_V + st, n);
-                issued = it + 1;
-                if (!STATES_ONLY && it >= 2) {
-                    // the outputs of chunk it - 2 leave the q tile, then it is loaded again
-                    if (!wait(OUT_READY + st, (it >> 1) - 1)) break;
-                    const int t = chunk_at(it - 2) * kC;
-                    tma_store_4d(&maps.out[ip], sb + SM_Q + st * kTile, 0, h, t, b);
-                    tma_store_4d(&maps.out[ip], sb + SM_Q + st * kTile + kHalf, 64, h, t, b);
-                    bulk_commit();
-                    bulk_wait_read();
-                    load(&maps.q[ip], sb + SM_Q + st * kTile, FULL_Q + st, n);
+            int it = 0;
+            for (; it < nsteps; ++it) {
+                const int st = it & 1, j = it < nown ? it : it - nown, t = chunk_at(j) * kC;
+                if (it >= 2) {                                  // the first two are under way
+                    if (!wait(FREE_K + st, (it >> 1) - 1)) break;
+                    load_tile(&maps.k[ip], sb + SM_K + st * kTile, bar(FULL_K + st), h, t, b);
+                    if (!wait(FREE_V + st, (it >> 1) - 1)) break;
+                    load_tile(&maps.v[ip], sb + SM_V + st * kTile, bar(FULL_V + st), h, t, b);
+                }
+                if (it >= nown && (it >= 2 || nown > 0)) {
+                    if (j >= 2) {
+                        // the outputs of chunk j - 2 leave the q tile, then it is loaded again
+                        if (!wait(OUT_READY + (j & 1), (j >> 1) - 1)) break;
+                        store(j - 2);
+                        bulk_wait_read();
+                    }
+                    if (it >= 2) load_tile(&maps.q[ip], sb + SM_Q + (j & 1) * kTile, bar(FULL_Q + (j & 1)), h, t, b);
                 }
             }
-            if (!STATES_ONLY)
-                for (int it = max(nchunks - 2, 0); it < nchunks && ok; ++it) {
-                    const int st = it & 1, t = chunk_at(it) * kC;
-                    if (!wait(OUT_READY + st, it >> 1)) break;
-                    tma_store_4d(&maps.out[ip], sb + SM_Q + st * kTile, 0, h, t, b);
-                    tma_store_4d(&maps.out[ip], sb + SM_Q + st * kTile + kHalf, 64, h, t, b);
-                    bulk_commit();
-                }
+            for (int j = max(nchunks - 2, 0); j < nchunks && ok; ++j) {
+                if (!wait(OUT_READY + (j & 1), j >> 1)) break;
+                store(j);
+            }
             bulk_wait_read();
             if (!ok)                        // no copy may land after the CTA has left
-                for (int it = max(issued - 2, 0); it < issued; ++it) {
-                    mbar_wait(bar(FULL_K + (it & 1)), (it >> 1) & 1);
-                    mbar_wait(bar(FULL_V + (it & 1)), (it >> 1) & 1);
-                    if (!STATES_ONLY) mbar_wait(bar(FULL_Q + (it & 1)), (it >> 1) & 1);
+                for (int i = max(it - 2, 0); i <= it && i < nsteps; ++i) {
+                    mbar_wait(bar(FULL_K + (i & 1)), (i >> 1) & 1);
+                    mbar_wait(bar(FULL_V + (i & 1)), (i >> 1) & 1);
+                    if (i >= nown) mbar_wait(bar(FULL_Q + ((i - nown) & 1)), ((i - nown) >> 1) & 1);
                 }
         }
     } else if (warp == kMmaWarp) {
         // Whole warps walk the loops and one elected lane issues, so that descriptors stay in
         // uniform registers: under `lane == 0` each product took 100 cycles to issue, against
         // the 64 it runs.
-        if (!STATES_ONLY) {
-            const uint32_t dq = desc_lo(sb + SM_Q, 16), dk = desc_lo(sb + SM_K, 16);
-            const uint32_t dv = desc_lo(sb + SM_V, kHalf), ds = desc_lo(sb + SM_S0, kHalf);
-            // A K step of 16 channels is 32 bytes inside the swizzled rows of a K-major tile, 16
-            // rows of an MN-major one (addresses in 16 bytes).
-            auto k_major = [](int ks) { return (uint32_t)((ks >> 2) * (kHalf >> 4) + (ks & 3) * 2); };
-            for (int it = 0; it < nchunks; ++it) {
-                const int st = it & 1;
-                const uint32_t stage = (uint32_t)st * (kTile >> 4);
-                // S = Q K^T
-                if (!wait_warp(FULL_Q + st, it >> 1) || !wait_warp(FULL_K + st, it >> 1)) break;
-                if (it > 0 && !wait_warp(PV_DONE, it - 1)) break;
-                tc_fence_after();
-                if (elect_one()) {
+        const uint32_t dq = desc_lo(sb + SM_Q, 16), dk = desc_lo(sb + SM_K, 16);
+        const uint32_t dv = desc_lo(sb + SM_V, kHalf), ds = desc_lo(sb + SM_S0, kHalf);
+        // A K step of 16 channels is 32 bytes inside the swizzled rows of a K-major tile, 16
+        // rows of an MN-major one (addresses in 16 bytes).
+        auto k_major = [](int ks) { return (uint32_t)((ks >> 2) * (kHalf >> 4) + (ks & 3) * 2); };
+        for (int j = 0; j < nchunks; ++j) {
+            const int it = nown + j, st = it & 1;
+            const uint32_t qs = (uint32_t)(j & 1) * (kTile >> 4), stage = (uint32_t)st * (kTile >> 4);
+            // S = Q K^T
+            if (!wait_warp(FULL_Q + (j & 1), j >> 1) || !wait_warp(FULL_K + st, it >> 1)) break;
+            if (j > 0 && !wait_warp(PV_DONE, j - 1)) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_ss(tm + TM_S, dq + stage + k_major(ks), dk + stage + k_major(ks), id_nt, ks > 0);
-                    umma_commit(bar(S_READY));
-                    umma_commit(bar(FREE_K + st));
-                }
-                // O = Q S0
-                if (!wait_warp(S0_READY, it) || (it > 0 && !wait_warp(O_FREE, it - 1))) break;
-                tc_fence_after();
-                if (elect_one()) {
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_ss(tm + TM_S, dq + qs + k_major(ks), dk + stage + k_major(ks), id_nt, ks > 0);
+                umma_commit(bar(S_READY));
+                umma_commit(bar(FREE_K + st));
+            }
+            // O = Q S0 (its columns were U's before: the state is published after the last of those)
+            if (!wait_warp(S0_READY, j) || (j > 0 && !wait_warp(O_FREE, j - 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_ss(tm + TM_O, dq + stage + k_major(ks), ds + (uint32_t)(ks * 128), id_nn, ks > 0);
-                    umma_commit(bar(QS_READY));
-                }
-                // O += P V
-                if (!wait_warp(FULL_V + st, it >> 1) || !wait_warp(PV_GO, it)) break;
-                tc_fence_after();
-                if (elect_one()) {
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_ss(tm + TM_O, dq + qs + k_major(ks), ds + (uint32_t)(ks * 128), id_nn, ks > 0);
+                umma_commit(bar(QS_READY));
+            }
+            // O += P V
+            if (!wait_warp(FULL_V + st, it >> 1) || !wait_warp(PV_GO, j)) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_ts(tm + TM_O, tm + TM_P + 8 * ks, dv + stage + (uint32_t)(ks * 128), id_nn, true);
-                    umma_commit(bar(PV_DONE));
-                    umma_commit(bar(FREE_V + st));
-                }
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_ts(tm + TM_O, tm + TM_P + 8 * ks, dv + stage + (uint32_t)(ks * 128), id_nn, true);
+                umma_commit(bar(PV_DONE));
+                umma_commit(bar(FREE_V + st));
             }
         }
     } else {
-        // U = K'^T V: a K step of three parts per slot
+        // U = K'^T V: a K step of three (or two) parts per slot
         const uint32_t dv = desc_lo(sb + SM_V, kHalf);
+        const int three_own = three_from(ps.sT), three_out = nown + three_from(ps.sT && seg == a.nseg - 1);
         int slot = 0, use = 0;
-        for (int it = 0; it < nchunks; ++it) {
-            const int st = it & 1;
-            const uint32_t v = dv + (uint32_t)st * (kTile >> 4);
+        for (int it = 0; it < nsteps; ++it) {
+            const bool own = it < nown;
+            const int st = it & 1, ub = own ? it & 1 : 0, uuse = own ? it >> 1 : ((nown + 1) >> 1) + it - nown;
+            const uint32_t v = dv + (uint32_t)st * (kTile >> 4), u = tm + (ub ? TM_O : TM_U);
+            const bool three = it >= (own ? three_own : three_out);
             if (!wait_warp(FULL_V + st, it >> 1)) break;
-            const int ub = STATES_ONLY ? it & 1 : 0;
-            const uint32_t u = tm + (ub ? TM_O : TM_U);
-            if (STATES_ONLY ? it >= 2 && !wait_warp(U_FREE + ub, (it >> 1) - 1) : it > 0 && !wait_warp(U_FREE, it - 1)) break;
+            if (uuse > 0 && !wait_warp(U_FREE + ub, uuse - 1)) break;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 if (!wait_warp(KP_READY + slot, use)) break;
@@ -571,16 +701,20 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 if (elect_one()) {
 #pragma unroll
                     for (int p = 0; p < 3; ++p)
-                        if (p < 2 || it >= three_at)
-                            umma_ts(u, tm + kp_column(slot) + p * kKpPart, v + (uint32_t)(ks * 128), id_nn,
+                        if (p < 2 || three)
+                            umma_ts(u, tm + TM_KP + slot * kKpSlot + p * kKpPart, v + (uint32_t)(ks * 128), id_nn,
                                     ks > 0 || p > 0);
                     umma_commit(bar(KP_FREE + slot));
                     if (ks == 7) {
                         umma_commit(bar(U_READY + ub));
                         umma_commit(bar(FREE_V + st));
+                        if (own) {                              // no other product reads these tiles
+                            mbar_arrive(bar(FREE_V + st));
+                            mbar_arrive(bar(FREE_K + st));
+                        }
                     }
                 }
-                if (++slot == kSlots) { slot = 0; ++use; }
+                if (++slot == kKpSlots) { slot = 0; ++use; }
             }
             if (!ok) break;
         }
@@ -629,36 +763,45 @@ cudaError_t token_map(const LaArgs &a, const void *p, CUtensorMap *m)
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename Kernel>
-int launch_registers(Kernel kernel)
+int launch_registers()
 {
     cudaFuncAttributes attr;
-    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : -1;
+    return cudaFuncGetAttributes(&attr, la_tc_kernel) == cudaSuccess ? attr.numRegs : -1;
 }
 
 }  // namespace
 
 bool la_tc_supported(int dk, int dv, kda_dtype dtype) { return dtype == KDA_BF16 && dk == kD && dv == kD; }
 
-cudaError_t launch_la_tc(const LaArgs &a, bool states_only, cudaStream_t stream)
+size_t la_tc_workspace_bytes(const LaArgs &a)
+{
+    return a.nseg > 1 ? flag_bytes(a) + sizeof(float) * kSlotFloats * a.npass * a.B * a.H * a.nseg : 0;
+}
+
+cudaError_t launch_la_tc(const LaArgs &a, cudaStream_t stream)
 {
     LaMaps maps;
     cudaError_t e = cudaSuccess;
     for (int i = 0; i < a.npass && e == cudaSuccess; ++i) {
-        e = token_map(a, a.pass[i].k, &maps.k[i]);
+        e = token_map(a, a.pass[i].q, &maps.q[i]);
+        if (e == cudaSuccess) e = token_map(a, a.pass[i].k, &maps.k[i]);
         if (e == cudaSuccess) e = token_map(a, a.pass[i].v, &maps.v[i]);
-        if (e == cudaSuccess && !states_only) e = token_map(a, a.pass[i].q, &maps.q[i]);
-        if (e == cudaSuccess && !states_only) e = token_map(a, a.pass[i].out, &maps.out[i]);
+        if (e == cudaSuccess) e = token_map(a, a.pass[i].out, &maps.out[i]);
     }
     if (e != cudaSuccess) return e;
-    auto kernel = states_only ? la_tc_kernel<true> : la_tc_kernel<false>;
     // the move of registers between warps is sized for this many: with fewer it would wait for ever
-    static const int regs[2] = {launch_registers(la_tc_kernel<false>), launch_registers(la_tc_kernel<true>)};
-    if (regs[states_only] != kLaunchRegs) return cudaErrorInvalidKernelImage;
-    static OncePerDevice once[2];
-    if ((e = set_shared_memory(kernel, (int)SM_TOTAL, once[states_only])) != cudaSuccess) return e;
-    const size_t grid = (size_t)a.npass * a.B * a.H * (states_only ? a.nseg - 1 : a.nseg);
-    kernel<<<(unsigned)grid, kThreads, SM_TOTAL, stream>>>(a, maps);
+    static const int regs = launch_registers();
+    if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    static OncePerDevice once;
+    if ((e = set_shared_memory(la_tc_kernel, (int)SM_TOTAL, once)) != cudaSuccess) return e;
+    int *flags = reinterpret_cast<int *>(a.ws);
+    float *slots = nullptr;
+    if (a.nseg > 1) {
+        if ((e = cudaMemsetAsync(flags, 0, flag_bytes(a), stream)) != cudaSuccess) return e;
+        slots = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(a.ws) + flag_bytes(a));
+    }
+    const size_t grid = (size_t)a.npass * a.B * a.H * a.nseg;
+    la_tc_kernel<<<(unsigned)grid, kThreads, SM_TOTAL, stream>>>(a, maps, flags, slots);
     e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
     return e;
