@@ -611,7 +611,7 @@ def _la_workspace(fn, q, dk, dv, code, workspace, where):
         n = fn(B, T, H, dk, dv, code)
         if not n:
             return None, 0, None
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(n, dtype=torch.uint8)
         return workspace.data_ptr(), n, workspace
     _need_workspace(workspace, q.device, where)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
@@ -656,9 +656,9 @@ def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=
     code = _need_la(q, k, v, log_decay, "kda_la_forward", (initial_state, "initial_state", state, torch.float32),
                     (out, "out", (B, T, H, dv), None), (final_state, "final_state", state, torch.float32))
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(v)
     if final_state is None and return_final_state:
-        final_state = torch.empty(state, dtype=torch.float32, device=q.device)
+        final_state = q.new_empty(state, dtype=torch.float32)
     ws, nbytes, _hold = _la_workspace(lib.kda_la_forward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_forward")
     st = _launch(q.get_device(), lib.kda_la_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
                  _address(initial_state), out.data_ptr(), _address(final_state), B, T, H, dk, dv, code, scale, ws, nbytes)
@@ -684,7 +684,7 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
                     (initial_state, "initial_state", state, torch.float32),
                     (grad_final_state, "grad_final_state", state, torch.float32))
     dq, dkey, dval = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ds0 = torch.empty(state, dtype=torch.float32, device=q.device) if initial_state_grad else None
+    ds0 = q.new_empty(state, dtype=torch.float32) if initial_state_grad else None
     ws, nbytes, _hold = _la_workspace(lib.kda_la_backward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_backward")
     st = _launch(q.get_device(), lib.kda_la_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
                  _address(initial_state), grad_out.data_ptr(), _address(grad_final_state), dq.data_ptr(),
@@ -729,7 +729,7 @@ def la_decode_step(q, k, v, log_decay, state, *, out=None, scale: float = 0.0):
     code = _need_la(q, k, v, log_decay, "kda_la_decode_step", (state, "state", (B, H, dk, dv), torch.float32),
                     (out, "out", (B, H, dv), None))
     if out is None:
-        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(v)
     st = _launch(q.get_device(), lib.kda_la_decode_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
                  state.data_ptr(), out.data_ptr(), B, H, dk, dv, code, scale)
     if st:
@@ -771,10 +771,10 @@ def paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths, *, out=No
                (block_table, "block_table", (B, max_pages), torch.int32), (lengths, "lengths", (B,), torch.int32),
                (out, "out", (B, H, D), None)))
     if out is None:
-        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     if workspace is None:
         nbytes = lib.kda_paged_decode_workspace_bytes(H, Hkv, D, code)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(nbytes, dtype=torch.uint8)
     else:
         _need_workspace(workspace, q.device, "kda_paged_decode_step")
         nbytes = workspace.numel() * workspace.element_size()

@@ -24,10 +24,10 @@
 // kernel runs into the power limit (1.5 of 1.97 GHz at B4 H32 T16384, 980 W), and U is half
 // of its products.
 //
-// Warps: 0-3 turn S into P, rescale O and write the outputs (a thread is a token); 4-11 make
-// K'^T in tensor memory, the two groups of four by turns (ldmatrix transposes the K tile);
-// 12-19 carry the state (a thread is a key channel and half of the value columns); 20 moves
-// tiles by TMA; 21 issues Q K^T, Q S0 and P V, 22 the steps of U: a wait and an issue take a
+// Warps: 0-3 turn S into P and 4-7 rescale O and write the outputs (a thread is a token); 8-15
+// make K'^T in tensor memory, the two groups of four by turns (ldmatrix transposes the K tile);
+// 16-23 carry the state (a thread is a key channel and half of the value columns); 24 moves
+// tiles by TMA; 25 issues Q K^T, Q S0 and P V, 26 the steps of U: a wait and an issue take a
 // warp about as long as the tensor core takes for a step.
 // Shared memory holds two stages of q, k, v (192 KB) and the state as an operand (32 KB); the
 // outputs of a chunk leave through its q tile.  Tiles are two boxes of 64 channels x 128
@@ -50,10 +50,17 @@ using namespace tcx;
 
 constexpr int kC = 128, kD = 128;
 constexpr int kRowWarps = 4, kKeyWarps = 8, kStateWarps = 8;
-constexpr int kStateWarp0 = kRowWarps + kKeyWarps, kTmaWarp = kStateWarp0 + kStateWarps, kMmaWarp = kTmaWarp + 1, kUpdateWarp = kMmaWarp + 1;
+constexpr int kKeyWarp0 = 2 * kRowWarps, kStateWarp0 = kKeyWarp0 + kKeyWarps, kTmaWarp = kStateWarp0 + kStateWarps, kMmaWarp = kTmaWarp + 1, kUpdateWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kUpdateWarp + 1);
-constexpr int kLaunchRegs = 80, kKeyRegs = 56, kStateRegs = 104;
-static_assert(kKeyWarps * (kLaunchRegs - kKeyRegs) >= kStateWarps * (kStateRegs - kLaunchRegs), "registers moved");
+#ifndef LA_SR
+#define LA_SR 96
+#define LA_PR 56
+#define LA_OR 64
+#define LA_KR 56
+#endif
+constexpr int kLaunchRegs = 72, kScoreRegs = LA_PR, kOutRegs = LA_OR, kKeyRegs = LA_KR, kStateRegs = LA_SR;
+static_assert(kRowWarps * (2 * kLaunchRegs - kScoreRegs - kOutRegs) + kKeyWarps * (kLaunchRegs - kKeyRegs) >=
+              kStateWarps * (kStateRegs - kLaunchRegs), "registers moved");
 
 // shared memory
 constexpr uint32_t kHalf = 64 * kC * 2, kTile = 2 * kHalf;        // 16 KB box, 32 KB tile
@@ -175,7 +182,7 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// Registers move from the key warps to the state warps, within what the block was launched with.
+// Registers move to the state warps from the others, within what the block was launched with.
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
 
@@ -250,20 +257,25 @@ __device__ __forceinline__ void load_initial(const LaArgs &a, int x, bool zero, 
 #pragma unroll
     for (int c0 = 0; c0 < 64; c0 += 32) {
         __syncwarp();
-#pragma unroll 2
-        for (int i = 0; i < 8; ++i) {
-            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-            uint32_t dst;
-            if (s0 && ps.s0_transposed) {                   // lane = row, four columns of it
+        if (!s0) {
+            if (c0 == 0)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) st_shared16(mine + 16u * (uint32_t)i, 0u, 0u, 0u, 0u);
+        } else if (ps.s0_transposed) {                      // lane = row, four columns of it
+#pragma unroll 4
+            for (int i = 0; i < 8; ++i) {
                 const float *p = s0 + (64 * part + c0 + 4 * i) * kD + 32 * quad + lane;
-                u = make_float4(p[0], p[kD], p[2 * kD], p[3 * kD]);
-                dst = mine + ((16u * (uint32_t)i) ^ swz);
-            } else {                                        // eight lanes = 128 bytes of a row
-                const int row = 4 * i + (lane >> 3), piece = lane & 7;
-                if (s0) u = *reinterpret_cast<const float4 *>(s0 + (32 * quad + row) * kD + 64 * part + c0 + 4 * piece);
-                dst = buf + (uint32_t)(row * 128) + ((16u * (uint32_t)piece) ^ ((uint32_t)(row & 7) << 4));
+                st_shared16(mine + ((16u * (uint32_t)i) ^ swz), __float_as_uint(p[0]), __float_as_uint(p[kD]),
+                            __float_as_uint(p[2 * kD]), __float_as_uint(p[3 * kD]));
             }
-            st_shared16(dst, __float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(u.z), __float_as_uint(u.w));
+        } else {                                            // eight lanes = 128 bytes of a row
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = 4 * i + (lane >> 3), piece = lane & 7;
+                const uint4 u = *reinterpret_cast<const uint4 *>(s0 + (32 * quad + row) * kD + 64 * part + c0 + 4 * piece);
+                st_shared16(buf + (uint32_t)(row * 128) + ((16u * (uint32_t)piece) ^ ((uint32_t)(row & 7) << 4)), u.x, u.y,
+                            u.z, u.w);
+            }
         }
         __syncwarp();
 #pragma unroll
@@ -348,7 +360,8 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         for (int i = 0; i < kBars; ++i) {
             const int count = (i >= FREE_K && i < FREE_V) ? kKeyWarps + 1
                               : (i >= FREE_V && i < OUT_READY) ? 2
-                              : (i >= OUT_READY && i < U_READY) || i == PV_GO || i == O_FREE ? kRowWarps
+                              : (i >= OUT_READY && i < U_READY) || i == O_FREE ? kRowWarps
+                              : i == PV_GO ? 2 * kRowWarps
                               : (i >= KP_READY && i < KP_FREE) ? kKeyWarps / 2
                               : (i >= U_FREE && i < KP_READY) || i == S0_READY ? kStateWarps : 1;
             mbar_init(bar(i), (uint32_t)count);
@@ -431,34 +444,45 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     };
 
     if (warp < kRowWarps) {
-        const float *sWP = reinterpret_cast<const float *>(smem + SM_WP), *sPW = reinterpret_cast<const float *>(smem + SM_PW);
+        // ---- P from S: token i
+        reg_dec<kScoreRegs>();
         const int i = 32 * warp + lane;
         const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
+        const float *w = reinterpret_cast<const float *>(smem + SM_WP) + 127 + i;
         for (int j = 0; j < nchunks; ++j) {
-            const int c = j == tail_at ? c_last : kC, st = j & 1;
-            // ---- P from S
             if (!wait_warp(S_READY, j)) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < 4; ++cb) {
                 uint32_t p[16];
                 if (rev ? cb >= warp : cb <= warp) {
                     float s[32];
                     tmem_ld32(row + TM_S + 32 * cb, s);
-                    const float *w = sWP + 127 + i - 32 * cb;
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) p[x] = pack_bf16(s[2 * x] * w[-2 * x], s[2 * x + 1] * w[-2 * x - 1]);
+                    for (int x = 0; x < 16; ++x)
+                        p[x] = pack_bf16(s[2 * x] * w[-32 * cb - 2 * x], s[2 * x + 1] * w[-32 * cb - 2 * x - 1]);
                 } else {
 #pragma unroll
                     for (int x = 0; x < 16; ++x) p[x] = 0u;
                 }
                 tmem_st16u(row + TM_P + 16 * cb, p);
             }
-            // ---- O <- f_inter lambda^(.) O
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(PV_GO);
+        }
+    } else if (warp < kKeyWarp0) {
+        // ---- O <- f_inter lambda^(.) O for P V to add to, then the outputs: token i
+        reg_dec<kOutRegs>();
+        const int i = 32 * (warp - kRowWarps) + lane;
+        const uint32_t row = tm + ((uint32_t)(32 * (warp - kRowWarps)) << 16);
+        const float *sPW = reinterpret_cast<const float *>(smem + SM_PW);
+        for (int j = 0; j < nchunks; ++j) {
+            const int c = j == tail_at ? c_last : kC, st = j & 1;
+            const float f = ps.f_inter * sPW[rev ? max(c - 1 - i, 0) : i + 1];
             if (!wait_warp(QS_READY, j)) break;
             tc_fence_after();
-            const float f = ps.f_inter * sPW[rev ? max(c - 1 - i, 0) : i + 1];
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < 8; ++cb) {
                 float o[16];
                 tmem_ld16(row + TM_O + 16 * cb, o);
@@ -469,11 +493,10 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(PV_GO);
-            // ---- outputs through the q tile
             if (!wait_warp(PV_DONE, j)) break;
             tc_fence_after();
             const uint32_t dst = sb + SM_Q + (uint32_t)(st * kTile + i * 128);
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < 4; ++cb) {
                 float o[32];
                 tmem_ld32(row + TM_O + 32 * cb, o);
@@ -484,19 +507,23 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                                 pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
             }
             tc_fence_before();
+            arrive_warp(O_FREE);                                // Q S0 of the next chunk may begin
             proxy_fence();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(O_FREE));
-                mbar_arrive(bar(OUT_READY + st));
-            }
+            arrive_warp(OUT_READY + st);
         }
     } else if (warp < kStateWarp0) {
         // ---- K'^T: slots of 16 tokens, this group's every second one; 32 key channels a warp
-        const int quad = warp & 3, group = (warp - kRowWarps) >> 2;
+        const int quad = warp & 3, group = (warp - kKeyWarp0) >> 2;
         const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_KP;
-        int slot = group, use = 0;                              // of the ring: every second one
+        int slot = group, use = 0, stored = -1;                 // of the ring: every second one
         reg_dec<kKeyRegs>();
+        auto hand_over = [&] {
+            if (stored < 0) return;
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(KP_READY + stored);
+            stored = -1;
+        };
         // ldmatrix: lanes 8 m .. 8 m + 7 name the rows (tokens) of matrix m: tokens 8 (m / 2) ..,
         // channels 8 (m % 2) .. of the 16 of a half-warp; 16-byte pieces swizzled by token % 8
         const int jr = lane & 7, m = lane >> 3, piece = 4 * (quad & 1) + (m & 1);
@@ -523,6 +550,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     if (three) cut3(x, hi[e], mid[e], lo[e]);
                     else split_pair2(x, hi[e], mid[e]);
                 }
+                hand_over();                                    // the slot before, stored meanwhile
                 if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) break;
                 tc_fence_after();
 #pragma unroll
@@ -532,15 +560,14 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     tmem_st_16x8(dst + kKpPart, mid[e], mid[e + 1], mid[e + 2], mid[e + 3]);
                     if (three) tmem_st_16x8(dst + 2 * kKpPart, lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive_warp(KP_READY + slot);
+                stored = slot;
                 slot += 2;
                 if (slot >= kKpSlots) { slot -= kKpSlots; ++use; }
             }
             if (!ok) break;
             arrive_warp(FREE_K + st);
         }
+        hand_over();
     } else if (warp < kTmaWarp) {
         // ---- the state: key channel r, value columns 64 part ..  (The walk leaves no registers for
         // what is needed before and after it: that is read from the work item again.)
@@ -694,7 +721,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
             const bool three = it >= (own ? three_own : three_out);
             if (!wait_warp(FULL_V + st, it >> 1)) break;
             if (uuse > 0 && !wait_warp(U_FREE + ub, uuse - 1)) break;
-#pragma unroll
+#pragma unroll 1
             for (int ks = 0; ks < 8; ++ks) {
                 if (!wait_warp(KP_READY + slot, use)) break;
                 tc_fence_after();
