@@ -515,15 +515,8 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         // ---- K'^T: slots of 16 tokens, this group's every second one; 32 key channels a warp
         const int quad = warp & 3, group = (warp - kKeyWarp0) >> 2;
         const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_KP;
-        int slot = group, use = 0, stored = -1;                 // of the ring: every second one
+        int slot = group, use = 0;                              // of the ring: every second one
         reg_dec<kKeyRegs>();
-        auto hand_over = [&] {
-            if (stored < 0) return;
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(KP_READY + stored);
-            stored = -1;
-        };
         // ldmatrix: lanes 8 m .. 8 m + 7 name the rows (tokens) of matrix m: tokens 8 (m / 2) ..,
         // channels 8 (m % 2) .. of the 16 of a half-warp; 16-byte pieces swizzled by token % 8
         const int jr = lane & 7, m = lane >> 3, piece = 4 * (quad & 1) + (m & 1);
@@ -538,19 +531,18 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
             if (!wait_warp(FULL_K + st, it >> 1)) break;
 #pragma unroll 1
             for (int s4 = 0; s4 < 4; ++s4) {
-                const float2 w0 = *reinterpret_cast<const float2 *>(wk + 32 * s4);
-                const float2 w1 = *reinterpret_cast<const float2 *>(wk + 32 * s4 + 8);
                 const uint32_t src = kt + st * kTile + s4 * (32 * 128);
                 uint32_t k0[4], k1[4], hi[8], mid[8], lo[8];
                 ldmatrix4_trans(src + off0, k0);
                 ldmatrix4_trans(src + off1, k1);
+                const float2 w0 = *reinterpret_cast<const float2 *>(wk + 32 * s4);
+                const float2 w1 = *reinterpret_cast<const float2 *>(wk + 32 * s4 + 8);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float2 x = scale_pair(e < 4 ? k0[e & 3] : k1[e & 3], (e & 2) ? w1 : w0);
                     if (three) cut3(x, hi[e], mid[e], lo[e]);
                     else split_pair2(x, hi[e], mid[e]);
                 }
-                hand_over();                                    // the slot before, stored meanwhile
                 if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) break;
                 tc_fence_after();
 #pragma unroll
@@ -560,14 +552,15 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     tmem_st_16x8(dst + kKpPart, mid[e], mid[e + 1], mid[e + 2], mid[e + 3]);
                     if (three) tmem_st_16x8(dst + 2 * kKpPart, lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
                 }
-                stored = slot;
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(KP_READY + slot);
                 slot += 2;
                 if (slot >= kKpSlots) { slot -= kKpSlots; ++use; }
             }
             if (!ok) break;
             arrive_warp(FREE_K + st);
         }
-        hand_over();
     } else if (warp < kTmaWarp) {
         // ---- the state: key channel r, value columns 64 part ..  (The walk leaves no registers for
         // what is needed before and after it: that is read from the work item again.)
