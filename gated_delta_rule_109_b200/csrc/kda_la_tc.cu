@@ -25,7 +25,8 @@
 // of its products.
 //
 // Warps: 0-3 turn S into P and 4-7 rescale O and write the outputs (a thread is a token); 8-15
-// make K'^T in tensor memory, the two groups of four by turns (ldmatrix transposes the K tile);
+// make K'^T in tensor memory, groups of four by turns (ldmatrix transposes the K tile; while
+// there are no outputs, warps 0-7 help);
 // 16-23 carry the state (a thread is a key channel and half of the value columns); 24 moves
 // tiles by TMA; 25 issues Q K^T, Q S0 and P V, 26 the steps of U: a wait and an issue take a
 // warp about as long as the tensor core takes for a step.
@@ -52,15 +53,8 @@ constexpr int kC = 128, kD = 128;
 constexpr int kRowWarps = 4, kKeyWarps = 8, kStateWarps = 8;
 constexpr int kKeyWarp0 = 2 * kRowWarps, kStateWarp0 = kKeyWarp0 + kKeyWarps, kTmaWarp = kStateWarp0 + kStateWarps, kMmaWarp = kTmaWarp + 1, kUpdateWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kUpdateWarp + 1);
-#ifndef LA_SR
-#define LA_SR 96
-#define LA_PR 56
-#define LA_OR 64
-#define LA_KR 56
-#endif
-constexpr int kLaunchRegs = 72, kScoreRegs = LA_PR, kOutRegs = LA_OR, kKeyRegs = LA_KR, kStateRegs = LA_SR;
-static_assert(kRowWarps * (2 * kLaunchRegs - kScoreRegs - kOutRegs) + kKeyWarps * (kLaunchRegs - kKeyRegs) >=
-              kStateWarps * (kStateRegs - kLaunchRegs), "registers moved");
+constexpr int kLaunchRegs = 72, kWorkRegs = 56, kStateRegs = 104;      // the first kStateWarp0 warps, the state's
+static_assert(kStateWarp0 * (kLaunchRegs - kWorkRegs) >= kStateWarps * (kStateRegs - kLaunchRegs), "registers moved");
 
 // shared memory
 constexpr uint32_t kHalf = 64 * kC * 2, kTile = 2 * kHalf;        // 16 KB box, 32 KB tile
@@ -173,6 +167,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
 {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t mbar, uint32_t n)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(mbar), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ bool elect_one()
@@ -358,7 +357,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     // ---- barriers, tensor memory, the work item
     if (warp == kTmaWarp && lane == 0) {
         for (int i = 0; i < kBars; ++i) {
-            const int count = (i >= FREE_K && i < FREE_V) ? kKeyWarps + 1
+            const int count = (i >= FREE_K && i < FREE_V) ? kStateWarp0
                               : (i >= FREE_V && i < OUT_READY) ? 2
                               : (i >= OUT_READY && i < U_READY) || i == O_FREE ? kRowWarps
                               : i == PV_GO ? 2 * kRowWarps
@@ -443,111 +442,40 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         return min(max(nchunks - 2 - (int)floorf((fade - behind) * (1.f / kC)), 0), nchunks);
     };
 
-    if (warp < kRowWarps) {
-        // ---- P from S: token i
-        reg_dec<kScoreRegs>();
-        const int i = 32 * warp + lane;
-        const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
-        const float *w = reinterpret_cast<const float *>(smem + SM_WP) + 127 + i;
-        for (int j = 0; j < nchunks; ++j) {
-            if (!wait_warp(S_READY, j)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
-                uint32_t p[16];
-                if (rev ? cb >= warp : cb <= warp) {
-                    float s[32];
-                    tmem_ld32(row + TM_S + 32 * cb, s);
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        p[x] = pack_bf16(s[2 * x] * w[-32 * cb - 2 * x], s[2 * x + 1] * w[-32 * cb - 2 * x - 1]);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) p[x] = 0u;
-                }
-                tmem_st16u(row + TM_P + 16 * cb, p);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(PV_GO);
-        }
-    } else if (warp < kKeyWarp0) {
-        // ---- O <- f_inter lambda^(.) O for P V to add to, then the outputs: token i
-        reg_dec<kOutRegs>();
-        const int i = 32 * (warp - kRowWarps) + lane;
-        const uint32_t row = tm + ((uint32_t)(32 * (warp - kRowWarps)) << 16);
-        const float *sPW = reinterpret_cast<const float *>(smem + SM_PW);
-        for (int j = 0; j < nchunks; ++j) {
-            const int c = j == tail_at ? c_last : kC, st = j & 1;
-            const float f = ps.f_inter * sPW[rev ? max(c - 1 - i, 0) : i + 1];
-            if (!wait_warp(QS_READY, j)) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int cb = 0; cb < 8; ++cb) {
-                float o[16];
-                tmem_ld16(row + TM_O + 16 * cb, o);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] *= f;
-                tmem_st16(row + TM_O + 16 * cb, o);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(PV_GO);
-            if (!wait_warp(PV_DONE, j)) break;
-            tc_fence_after();
-            const uint32_t dst = sb + SM_Q + (uint32_t)(st * kTile + i * 128);
-#pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
-                float o[32];
-                tmem_ld32(row + TM_O + 32 * cb, o);
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    st_shared16(dst + (cb >> 1) * kHalf + (uint32_t)(((4 * (cb & 1) + x) ^ (i & 7)) << 4),
-                                pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
-                                pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
-            }
-            tc_fence_before();
-            arrive_warp(O_FREE);                                // Q S0 of the next chunk may begin
-            proxy_fence();
-            arrive_warp(OUT_READY + st);
-        }
-    } else if (warp < kStateWarp0) {
-        // ---- K'^T: slots of 16 tokens, this group's every second one; 32 key channels a warp
-        const int quad = warp & 3, group = (warp - kKeyWarp0) >> 2;
-        const uint32_t row = tm + ((uint32_t)(32 * quad) << 16) + TM_KP;
-        int slot = group, use = 0;                              // of the ring: every second one
-        reg_dec<kKeyRegs>();
+    if (warp < kStateWarp0) {
+        reg_dec<kWorkRegs>();
+        // ---- K'^T: 16 tokens a slot of the ring, 32 key channels a warp.  Of a step's eight slots
+        // group g of n makes g, g + n, ..
+        const int quad = warp & 3;
         // ldmatrix: lanes 8 m .. 8 m + 7 name the rows (tokens) of matrix m: tokens 8 (m / 2) ..,
         // channels 8 (m % 2) .. of the 16 of a half-warp; 16-byte pieces swizzled by token % 8
         const int jr = lane & 7, m = lane >> 3, piece = 4 * (quad & 1) + (m & 1);
-        const uint32_t kt = sb + SM_K + (quad >> 1) * kHalf + (uint32_t)((16 * group + 8 * (m >> 1) + jr) * 128);
+        const uint32_t kt = sb + SM_K + (quad >> 1) * kHalf + (uint32_t)((8 * (m >> 1) + jr) * 128);
         const uint32_t off0 = (uint32_t)((piece ^ jr) << 4), off1 = (uint32_t)(((piece + 2) ^ jr) << 4);
-        const float *sWK = reinterpret_cast<const float *>(smem + SM_WK) + 16 * group + 2 * (lane & 3);
-        const int three_own = three_from(ps.sT), three_out = nown + three_from(ps.sT && seg == a.nseg - 1);
-        for (int it = 0; it < nsteps; ++it) {
-            const int st = it & 1, j = it < nown ? it : it - nown;
-            const float *wk = sWK + (j == tail_at ? kC : 0);
-            const bool three = it >= (it < nown ? three_own : three_out);
-            if (!wait_warp(FULL_K + st, it >> 1)) break;
+        auto make_keys = [&](int it, int j, bool three, int group, int ngroups) {
+            const float *wk = reinterpret_cast<const float *>(smem + SM_WK) + (j == tail_at ? kC : 0) + 2 * (lane & 3);
+            const int st = it & 1;
+            if (!wait_warp(FULL_K + st, it >> 1)) return false;
 #pragma unroll 1
-            for (int s4 = 0; s4 < 4; ++s4) {
-                const uint32_t src = kt + st * kTile + s4 * (32 * 128);
+            for (int ks = group; ks < 8; ks += ngroups) {
+                const uint32_t src = kt + st * kTile + ks * (16 * 128);
+                const int use = (8 * it + ks) / kKpSlots, slot = 8 * it + ks - use * kKpSlots;
                 uint32_t k0[4], k1[4], hi[8], mid[8], lo[8];
                 ldmatrix4_trans(src + off0, k0);
                 ldmatrix4_trans(src + off1, k1);
-                const float2 w0 = *reinterpret_cast<const float2 *>(wk + 32 * s4);
-                const float2 w1 = *reinterpret_cast<const float2 *>(wk + 32 * s4 + 8);
+                const float2 w0 = *reinterpret_cast<const float2 *>(wk + 16 * ks);
+                const float2 w1 = *reinterpret_cast<const float2 *>(wk + 16 * ks + 8);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float2 x = scale_pair(e < 4 ? k0[e & 3] : k1[e & 3], (e & 2) ? w1 : w0);
                     if (three) cut3(x, hi[e], mid[e], lo[e]);
                     else split_pair2(x, hi[e], mid[e]);
                 }
-                if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) break;
+                if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int e = 0; e < 8; e += 4) {
-                    const uint32_t dst = row + ((uint32_t)(4 * e) << 16) + slot * kKpSlot;
+                    const uint32_t dst = tm + ((uint32_t)(32 * quad + 4 * e) << 16) + TM_KP + slot * kKpSlot;
                     tmem_st_16x8(dst, hi[e], hi[e + 1], hi[e + 2], hi[e + 3]);
                     tmem_st_16x8(dst + kKpPart, mid[e], mid[e + 1], mid[e + 2], mid[e + 3]);
                     if (three) tmem_st_16x8(dst + 2 * kKpPart, lo[e], lo[e + 1], lo[e + 2], lo[e + 3]);
@@ -555,11 +483,89 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 tmem_wait_st();
                 tc_fence_before();
                 arrive_warp(KP_READY + slot);
-                slot += 2;
-                if (slot >= kKpSlots) { slot -= kKpSlots; ++use; }
             }
-            if (!ok) break;
-            arrive_warp(FREE_K + st);
+            return true;
+        };
+        const int three_own = three_from(ps.sT);
+        for (int it = 0; it < nown; ++it) {
+            if (!make_keys(it, it, it >= three_own, warp >> 2, kStateWarp0 / 4)) break;
+            arrive_warp(FREE_K + (it & 1));
+        }
+        if (warp >= kKeyWarp0) {
+            const int three_out = three_from(ps.sT && seg == a.nseg - 1), group = (warp - kKeyWarp0) >> 2;
+            for (int j = 0; j < nchunks && ok; ++j) {
+                const int it = nown + j;
+                if (!make_keys(it, j, j >= three_out, group, kKeyWarps / 4)) break;
+                __syncwarp();
+                // the eight of these warps, Q K^T's commit, and one for the warps that do not read K here
+                if (lane == 0) mbar_arrive_n(bar(FREE_K + (it & 1)), warp == kKeyWarp0 ? kStateWarp0 - kKeyWarps : 1);
+            }
+        } else if (warp < kRowWarps) {
+            // ---- P from S: token i
+            const int i = 32 * warp + lane;
+            const uint32_t row = tm + ((uint32_t)(32 * warp) << 16);
+            const float *w = reinterpret_cast<const float *>(smem + SM_WP) + 127 + i;
+            for (int j = 0; j < nchunks && ok; ++j) {
+                if (!wait_warp(S_READY, j)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int cb = 0; cb < 4; ++cb) {
+                    uint32_t p[16];
+                    if (rev ? cb >= warp : cb <= warp) {
+                        float s[32];
+                        tmem_ld32(row + TM_S + 32 * cb, s);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x)
+                            p[x] = pack_bf16(s[2 * x] * w[-32 * cb - 2 * x], s[2 * x + 1] * w[-32 * cb - 2 * x - 1]);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) p[x] = 0u;
+                    }
+                    tmem_st16u(row + TM_P + 16 * cb, p);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(PV_GO);
+            }
+        } else {
+            // ---- O <- f_inter lambda^(.) O for P V to add to, then the outputs: token i
+            const int i = 32 * (warp - kRowWarps) + lane;
+            const uint32_t row = tm + ((uint32_t)(32 * (warp - kRowWarps)) << 16);
+            const float *sPW = reinterpret_cast<const float *>(smem + SM_PW);
+            for (int j = 0; j < nchunks && ok; ++j) {
+                const int c = j == tail_at ? c_last : kC, st = j & 1;
+                const float f = ps.f_inter * sPW[rev ? max(c - 1 - i, 0) : i + 1];
+                if (!wait_warp(QS_READY, j)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int cb = 0; cb < 8; ++cb) {
+                    float o[16];
+                    tmem_ld16(row + TM_O + 16 * cb, o);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) o[x] *= f;
+                    tmem_st16(row + TM_O + 16 * cb, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(PV_GO);
+                if (!wait_warp(PV_DONE, j)) break;
+                tc_fence_after();
+                const uint32_t dst = sb + SM_Q + (uint32_t)(st * kTile + i * 128);
+#pragma unroll 1
+                for (int cb = 0; cb < 4; ++cb) {
+                    float o[32];
+                    tmem_ld32(row + TM_O + 32 * cb, o);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        st_shared16(dst + (cb >> 1) * kHalf + (uint32_t)(((4 * (cb & 1) + x) ^ (i & 7)) << 4),
+                                    pack_bf16(o[8 * x], o[8 * x + 1]), pack_bf16(o[8 * x + 2], o[8 * x + 3]),
+                                    pack_bf16(o[8 * x + 4], o[8 * x + 5]), pack_bf16(o[8 * x + 6], o[8 * x + 7]));
+                }
+                tc_fence_before();
+                arrive_warp(O_FREE);                                // Q S0 of the next chunk may begin
+                proxy_fence();
+                arrive_warp(OUT_READY + st);
+            }
         }
     } else if (warp < kTmaWarp) {
         // ---- the state: key channel r, value columns 64 part ..  (The walk leaves no registers for
@@ -728,10 +734,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     if (ks == 7) {
                         umma_commit(bar(U_READY + ub));
                         umma_commit(bar(FREE_V + st));
-                        if (own) {                              // no other product reads these tiles
-                            mbar_arrive(bar(FREE_V + st));
-                            mbar_arrive(bar(FREE_K + st));
-                        }
+                        if (own) mbar_arrive(bar(FREE_V + st));         // no other product reads the tile
                     }
                 }
                 if (++slot == kKpSlots) { slot = 0; ++use; }
