@@ -5,8 +5,10 @@
 // resident in shared memory.  A chunk is four small products of register tiles:
 // 64 x 64 scores (4 x 4 a thread), the outputs P V + Q S (4 rows x DV/16 columns a
 // thread) and the state K'^T V (DK/16 x DV/16 a thread), operands read as 16-byte
-// vectors of padded rows.  Powers of lambda are computed in 64 bits once per CTA, so
-// their rounding does not grow along the sequence.
+// vectors of padded rows.  A chunk's 8 dk dv + .. multiply-adds are what bounds it (4.3 us a
+// chunk of 64-channel heads at the SM's full rate), so the tile loads of a chunk are all under
+// way together and two CTAs share an SM where they fit.  Powers of lambda are computed in 64
+// bits once per CTA, so their rounding does not grow along the sequence.
 #include "kda_la.cuh"
 
 namespace kda {
@@ -24,7 +26,8 @@ struct LaSmem {
     static constexpr int off_p = off_v + kC * PV;
     static constexpr int off_s = off_p + kC * PP;
     static constexpr int off_w = off_s + DK * PV;                 // lambda^n, n = 0..64
-    static constexpr int total = off_w + kC + 4;
+    static constexpr int off_l = off_w + kC + 4;                  // lambda^c of a whole and of the ragged chunk, two floats each
+    static constexpr int total = off_l + 4;
     static constexpr size_t bytes = sizeof(float) * (size_t)total;
 };
 
@@ -38,8 +41,40 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float acc)
     return acc;
 }
 
+// R rows of D channels, one per token t (zeros from c on), to shared memory as fp32.  The loads
+// are all issued before the first is needed.
+template <int D>
+__device__ __forceinline__ void stage(float *dst, const float *src, size_t token_stride, int c, int tid)
+{
+#pragma unroll
+    for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
+        const int id = e * kThreads + tid, t = id / (D / 4), x = 4 * (id % (D / 4));
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + t * (D + 4) + x);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     :: "r"(to), "l"(src + (t < c ? t * token_stride + x : 0)), "r"(t < c ? 16 : 0) : "memory");
+    }
+}
+template <int D>
+__device__ __forceinline__ void stage(float *dst, const __nv_bfloat16 *src, size_t token_stride, int c, int tid)
+{
+    float4 v[kC * D / 4 / kThreads];
+#pragma unroll
+    for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
+        const int id = e * kThreads + tid, t = id / (D / 4), x = 4 * (id % (D / 4));
+        v[e] = t < c ? la_load4(src + t * token_stride + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
+        const int id = e * kThreads + tid;
+        la_store4(dst + (id / (D / 4)) * (D + 4) + 4 * (id % (D / 4)), v[e]);
+    }
+}
+
+// CTAs of an SM: two where the shared memory of both fits
+template <int DK, int DV> constexpr int simt_resident() { return LaSmem<DK, DV>::bytes <= 112 * 1024 ? 2 : 1; }
+
 template <int DK, int DV, typename InT, bool STATES_ONLY>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, simt_resident<DK, DV>())
 la_simt_kernel(const __grid_constant__ LaArgs a)
 {
     using L = LaSmem<DK, DV>;
@@ -49,6 +84,7 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
     float *sQ = sm + L::off_q, *sK = sm + L::off_k, *sV = sm + L::off_v, *sP = sm + L::off_p, *sS = sm + L::off_s;
     float *sW = sm + L::off_w;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
     const int seg = blockIdx.x % nwork;
@@ -60,16 +96,50 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
     la_segment(seg, a.nseg, a.seg_tokens, a.T, rev, t_lo, t_hi);
     float *slots = a.nseg > 1 ? a.ws + ((size_t)ip * a.B * a.H + bh) * a.nseg * DK * DV : nullptr;
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // nothing is read before what is ahead has completed
     if (tid <= kC) sW[tid] = (float)la_power(a.log_decay, h, tid);
-    // ---- entering state
-    if (STATES_ONLY) {
-        for (int e = tid; e < DK * DV; e += kThreads) sS[(e / DV) * PV + e % DV] = 0.f;
+    else if (tid >= 96 && tid < 98) {
+        const double l = la_power(a.log_decay, h, tid == 96 ? kC : (t_hi - 1) % kC + 1);
+        sm[L::off_l + 2 * (tid - 96)] = (float)l;
+        sm[L::off_l + 2 * (tid - 96) + 1] = (float)(l - (double)(float)l);
+    }
+    // ---- entering state.  One segment, and segment 0 of the walk without outputs: the initial
+    // state (kept in slot nseg - 1 for the outputs of segment 0: final_state may be the same
+    // buffer).  Otherwise the earlier segments' contributions, each faded by the tokens between.
+    if (slots && !STATES_ONLY) {
+        __syncthreads();
+        float *weight = sP;                                     // [seg] pairs
+        if (tid < seg) {
+            int x0, x1;
+            la_segment(tid, a.nseg, a.seg_tokens, a.T, rev, x0, x1);
+            const double l = la_power(a.log_decay, h, rev ? x0 - t_hi : t_lo - x1);
+            weight[2 * tid] = (float)l;
+            weight[2 * tid + 1] = (float)(l - (double)(float)l);
+        }
+        __syncthreads();
+        for (int e = 4 * tid; e < DK * DV; e += 4 * kThreads) {
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (seg == 0) s = la_load4(slots + (size_t)(a.nseg - 1) * DK * DV + e);
+#pragma unroll 8
+            for (int g = 0; g < seg; ++g) {
+                const float4 u = la_load4(slots + (size_t)g * DK * DV + e);
+                fma4(s, weight[2 * g + 1], u);
+                fma4(s, weight[2 * g], u);
+            }
+            la_store4(sS + (e / DV) * PV + e % DV, s);
+        }
     } else {
-        const float *s0 = slots ? slots + (size_t)seg * DK * DV : ps.s0 ? ps.s0 + (size_t)bh * DK * DV : nullptr;
-        const bool tr = !slots && ps.s0_transposed;
-        for (int e = tid; e < DK * DV; e += kThreads) {
+        const float *s0 = ps.s0 && (!STATES_ONLY || seg == 0) ? ps.s0 + (size_t)bh * DK * DV : nullptr;
+#pragma unroll 4
+        for (int e = 4 * tid; e < DK * DV; e += 4 * kThreads) {
             const int r = e / DV, c = e % DV;
-            sS[r * PV + c] = s0 ? s0[tr ? c * DK + r : e] : 0.f;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s0) {
+                const float *p = s0 + (ps.s0_transposed ? c * DK + r : e);
+                s = ps.s0_transposed ? make_float4(p[0], p[DK], p[2 * DK], p[3 * DK]) : la_load4(p);
+            }
+            la_store4(sS + r * PV + c, s);
+            if (STATES_ONLY && seg == 0) la_store4(slots + (size_t)(a.nseg - 1) * DK * DV + e, s);
         }
     }
 
@@ -80,18 +150,11 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
         const int t0 = n * kC, c = min(kC, t_hi - t0);
         __syncthreads();                        // the chunk before is consumed
         // ---- stage q, k, v (rows past c are zero: they change nothing)
-        for (int e = tid; e < kC * DK / 4; e += kThreads) {
-            const int t = e / (DK / 4), x = 4 * (e % (DK / 4));
-            const size_t g = (((size_t)b * a.T + t0 + t) * a.H + h) * DK + x;
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!STATES_ONLY) la_store4(sQ + t * PK + x, t < c ? la_load4(q + g) : z);
-            la_store4(sK + t * PK + x, t < c ? la_load4(k + g) : z);
-        }
-        for (int e = tid; e < kC * DV / 4; e += kThreads) {
-            const int t = e / (DV / 4), x = 4 * (e % (DV / 4));
-            const size_t g = (((size_t)b * a.T + t0 + t) * a.H + h) * DV + x;
-            la_store4(sV + t * PV + x, t < c ? la_load4(v + g) : make_float4(0.f, 0.f, 0.f, 0.f));
-        }
+        const size_t at = ((size_t)b * a.T + t0) * a.H + h;
+        if (!STATES_ONLY) stage<DK>(sQ, q + at * DK, (size_t)a.H * DK, c, tid);
+        stage<DK>(sK, k + at * DK, (size_t)a.H * DK, c, tid);
+        stage<DV>(sV, v + at * DV, (size_t)a.H * DV, c, tid);
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
 
         if (!STATES_ONLY) {
@@ -197,8 +260,7 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
                 }
             }
         }
-        const double lc = la_power(a.log_decay, h, c);
-        const float hi = (float)lc, lo = (float)(lc - (double)hi);
+        const float hi = sm[L::off_l + (c == kC ? 0 : 2)], lo = sm[L::off_l + (c == kC ? 1 : 3)];
 #pragma unroll
         for (int r = 0; r < RK; ++r)
 #pragma unroll
@@ -212,10 +274,31 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
     }
     __syncthreads();
     // ---- leaving state
-    float *dst = STATES_ONLY ? slots + (size_t)(seg + 1) * DK * DV
+    float *dst = STATES_ONLY ? slots + (size_t)seg * DK * DV
                  : (seg == a.nseg - 1 && ps.sT) ? ps.sT + (size_t)bh * DK * DV : nullptr;
     if (dst)
-        for (int e = tid; e < DK * DV; e += kThreads) dst[e] = sS[(e / DV) * PV + e % DV];
+#pragma unroll 8
+        for (int e = 4 * tid; e < DK * DV; e += 4 * kThreads) la_store4(dst + e, la_load4(sS + (e / DV) * PV + e % DV));
+}
+
+// A launch that may begin while the kernel ahead of it ends (it waits for that one's results).
+template <typename Kernel>
+cudaError_t launch_behind(Kernel kernel, size_t grid, size_t smem, const LaArgs &a, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e == cudaSuccess) note_launch();
+    return e;
 }
 
 template <int DK, int DV, typename InT, bool STATES_ONLY>
@@ -227,10 +310,7 @@ cudaError_t launch_typed(const LaArgs &a, cudaStream_t stream)
     cudaError_t e = set_shared_memory(kernel, (int)bytes, once);
     if (e != cudaSuccess) return e;
     const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
-    kernel<<<(unsigned)((size_t)a.npass * a.B * a.H * nwork), kThreads, bytes, stream>>>(a);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) note_launch();
-    return e;
+    return launch_behind(kernel, (size_t)a.npass * a.B * a.H * nwork, bytes, a, stream);
 }
 
 template <typename InT, bool STATES_ONLY>
@@ -243,45 +323,8 @@ cudaError_t launch_dims(const LaArgs &a, cudaStream_t stream)
     return cudaErrorInvalidValue;
 }
 
-// Slot s of a (pass, b, h) holds segment s - 1's own state (slot 0: nothing); afterwards
-// it holds the state that enters segment s: S_0 the pass's initial state, then
-// S_s = lambda^(tokens of segment s - 1) S_{s-1} + slot s.  One thread per four elements.
-__global__ void __launch_bounds__(256)
-la_scan_kernel(const __grid_constant__ LaArgs a)
-{
-    const int quads = a.dk * a.dv / 4;
-    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
-    const size_t head = id / quads;
-    const int e = 4 * (int)(id % quads);
-    const int nbh = a.B * a.H;
-    if (head >= (size_t)a.npass * nbh) return;
-    const int ip = (int)(head / nbh), bh = (int)(head % nbh);
-    const LaPass &ps = a.pass[ip];
-    float *slot = a.ws + head * a.nseg * a.dk * a.dv + e;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ps.s0) {
-        const float *s0 = ps.s0 + (size_t)bh * a.dk * a.dv;
-        if (ps.s0_transposed) {
-            const float *p = s0 + (e % a.dv) * a.dk + e / a.dv;
-            s = make_float4(p[0], p[a.dk], p[2 * a.dk], p[3 * a.dk]);
-        } else s = *reinterpret_cast<const float4 *>(s0 + e);
-    }
-    *reinterpret_cast<float4 *>(slot) = s;
-    for (int g = 1; g < a.nseg; ++g) {
-        int t0, t1;
-        la_segment(g - 1, a.nseg, a.seg_tokens, a.T, ps.rev, t0, t1);
-        const double l = la_power(a.log_decay, bh % a.H, t1 - t0);
-        const float hi = (float)l, lo = (float)(l - (double)hi);
-        float *p = slot + (size_t)g * a.dk * a.dv;
-        float4 u = *reinterpret_cast<const float4 *>(p);
-        fma4(u, lo, s);
-        fma4(u, hi, s);
-        *reinterpret_cast<float4 *>(p) = s = u;
-    }
-}
-
-// fp32 arithmetic on CUDA cores.  states_only: each segment's state from zero goes to its slot
-// of a.ws, [npass][B * H][nseg][dk][dv] fp32, no outputs.
+// fp32 arithmetic on CUDA cores.  states_only: each segment's own contribution to the state
+// (all but the last's) goes to its slot of a.ws, [npass][B * H][nseg][dk][dv] fp32, no outputs.
 cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t stream)
 {
     if (a.dtype == KDA_BF16)
@@ -301,7 +344,8 @@ void la_choose_segments(LaArgs &a)
     constexpr int kSms = 148, kMaxSegments = 64;
     const bool tc = la_tc_supported(a.dk, a.dv, a.dtype);
     const int C = tc ? 128 : kC;
-    const double state_cost = tc ? 0.45 : 0.5, join_cost = tc ? 3.0 : 2.0, per_segment = tc ? 0.2 : 0.0;
+    const int places = 148 * (!tc && a.dk == 64 && a.dv == 64 ? simt_resident<64, 64>() : 1);
+    const double state_cost = tc ? 0.6 : 0.5, join_cost = tc ? 3.0 : 1.0, per_segment = tc ? 0.5 : 0.05;
     const int chunks = (a.T + C - 1) / C;
     const long long heads = (long long)a.npass * a.B * a.H;
     a.nseg = 1;
@@ -309,7 +353,7 @@ void la_choose_segments(LaArgs &a)
     double best = 0.0;
     for (int want = 1; want <= kMaxSegments && want <= chunks; ++want) {
         const int len = (chunks + want - 1) / want, n = (chunks + len - 1) / len;
-        const long long waves = (heads * n + kSms - 1) / kSms;
+        const long long waves = (heads * n + places - 1) / places;
         const double t = (double)waves * (n > 1 ? len * (1.0 + state_cost) + join_cost + per_segment * n : len);
         if (want == 1 || t < best) {
             best = t;
@@ -325,18 +369,13 @@ size_t la_workspace_bytes(const LaArgs &a)
     return a.nseg > 1 ? sizeof(float) * (size_t)a.npass * a.B * a.H * a.nseg * a.dk * a.dv : 0;
 }
 
-// CUDA cores with nseg > 1: every segment's own state, the scan over the segments, then the
-// outputs; else the outputs alone.
+// CUDA cores with nseg > 1: every segment's own contribution, then the outputs.
 cudaError_t launch_la(const LaArgs &a, cudaStream_t stream)
 {
     if (la_tc_supported(a.dk, a.dv, a.dtype)) return launch_la_tc(a, stream);
     if (a.nseg > 1) {
-        cudaError_t e = launch_la_simt(a, true, stream);
+        const cudaError_t e = launch_la_simt(a, true, stream);
         if (e != cudaSuccess) return e;
-        const size_t n = (size_t)a.npass * a.B * a.H * (a.dk * a.dv / 4);
-        la_scan_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        note_launch();
     }
     return launch_la_simt(a, false, stream);
 }
