@@ -341,7 +341,7 @@ cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t strea
 // the walk with outputs.
 void la_choose_segments(LaArgs &a)
 {
-    constexpr int kSms = 148, kMaxSegments = 64;
+    constexpr int kMaxSegments = 32;        // a warp's lanes look at them
     const bool tc = la_tc_supported(a.dk, a.dv, a.dtype);
     const int C = tc ? 128 : kC;
     const int places = 148 * (!tc && a.dk == 64 && a.dv == 64 ? simt_resident<64, 64>() : 1);
