@@ -205,6 +205,15 @@ __device__ __forceinline__ float2 scale_pair(uint32_t k, float2 w)
 {
     return mul2(make_float2(__uint_as_float(k << 16), __uint_as_float(k & 0xffff0000u)), w);
 }
+// k w as the sum of two bf16, k a pair of bf16 and w = wh + wl in two parts, in packed bf16
+// arithmetic: hi = k wh rounded, whose error k wh - hi has at most 8 bits and is exact, and
+// mid = k wl + that error, rounded.  Off by at most 2^-17 of k w; half the instructions of the
+// same in fp32.
+__device__ __forceinline__ void cut2(uint32_t k, uint32_t wh, uint32_t wl, uint32_t &hi, uint32_t &mid)
+{
+    asm("{\n\t.reg .b32 n;\n\tmul.rn.bf16x2 %0, %2, %3;\n\tneg.bf16x2 n, %0;\n\tfma.rn.bf16x2 n, %2, %3, n;\n\t"
+        "fma.rn.bf16x2 %1, %2, %4, n;\n\t}" : "=&r"(hi), "=r"(mid) : "r"(k), "r"(wh), "r"(wl));
+}
 // x as the sum of three bf16: its 24 bits cut into 8 + 8 + 8.
 __device__ __forceinline__ void cut3(float2 x, uint32_t &hi, uint32_t &mid, uint32_t &lo)
 {
@@ -465,11 +474,16 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 ldmatrix4_trans(src + off1, k1);
                 const float2 w0 = *reinterpret_cast<const float2 *>(wk + 16 * ks);
                 const float2 w1 = *reinterpret_cast<const float2 *>(wk + 16 * ks + 8);
+                if (three) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 x = scale_pair(e < 4 ? k0[e & 3] : k1[e & 3], (e & 2) ? w1 : w0);
-                    if (three) cut3(x, hi[e], mid[e], lo[e]);
-                    else split_pair2(x, hi[e], mid[e]);
+                    for (int e = 0; e < 8; ++e)
+                        cut3(scale_pair(e < 4 ? k0[e & 3] : k1[e & 3], (e & 2) ? w1 : w0), hi[e], mid[e], lo[e]);
+                } else {
+                    uint32_t wh[2], wl[2];
+                    split_pair2(w0, wh[0], wl[0]);
+                    split_pair2(w1, wh[1], wl[1]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) cut2(e < 4 ? k0[e & 3] : k1[e & 3], wh[(e >> 1) & 1], wl[(e >> 1) & 1], hi[e], mid[e]);
                 }
                 if (use > 0 && !wait_warp(KP_FREE + slot, use - 1)) return false;
                 tc_fence_after();
@@ -578,8 +592,8 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         // segment 0's own contribution includes the initial state
         const uint32_t buf = sb + SM_S0 + (uint32_t)(4096 * (4 * part + quad));     // until the state is published
         load_initial(a, reread(sb + SM_TMEM + 4), seg != 0, quad, part, lane, buf, S);
-        // S <- lambda^c S + U
-        auto absorb = [&](int ub, int use, int j) {
+        // S <- lambda^c S + U; the second float of lambda^c goes with the third part of K'
+        auto absorb = [&](int ub, int use, int j, bool exact) {
             if (!wait_warp(U_READY + ub, use)) return false;
             tc_fence_after();
             const float2 l = reinterpret_cast<const float2 *>(smem + SM_LC)[j == tail_at];
@@ -589,7 +603,10 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 float u[8];
                 tmem_ld8(src + x, u);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) S[x + y] = fmaf(l.x, S[x + y], fmaf(l.y, S[x + y], u[y]));
+                for (int y = 0; y < 8; ++y) {
+                    if (exact) u[y] = fmaf(l.y, S[x + y], u[y]);
+                    S[x + y] = fmaf(l.x, S[x + y], u[y]);
+                }
             }
             tc_fence_before();
             arrive_warp(U_FREE + ub);
@@ -608,8 +625,9 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         if (a.nseg > 1) {
             const int me = tid - 32 * kStateWarp0;
             if (seg == 0) leave_state(a, reread(sb + SM_TMEM + 4), a.nseg - 1, me, false, flags, slots, S);
+            const int three_own = three_from(ps.sT);
             for (int j = 0; j < nown; ++j)
-                if (!absorb(j & 1, j >> 1, j)) break;
+                if (!absorb(j & 1, j >> 1, j, j >= three_own)) break;
             if (ok) {
                 const int x0 = reread(sb + SM_TMEM + 4);
                 if (nown > 0) leave_state(a, x0, x0 / heads, me, true, flags, slots, S);
@@ -617,8 +635,9 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
             }
         }
         if (ok) publish();
+        const int three_out = three_from(ps.sT && seg == a.nseg - 1);
         for (int j = 0; j < nchunks && ok; ++j) {
-            if (!absorb(0, ((nown + 1) >> 1) + j, j)) break;
+            if (!absorb(0, ((nown + 1) >> 1) + j, j, j >= three_out)) break;
             if (j + 1 < nchunks) {
                 if (!wait_warp(QS_READY, j)) break;             // the operand of this chunk has been read
                 publish();
