@@ -29,6 +29,7 @@ LIB_PATH = os.path.join(_PKG, "libkda.so")
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_MISALIGNED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = range(6)
 KDA_BF16, KDA_F32 = 0, 1
+_CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
 KDA_PREP_LOGSIGMOID_GATE, KDA_PREP_L2NORM_QK = 1, 2
 
 # every symbol include/kda.h declares
@@ -159,14 +160,8 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _need_all(index: int, dtype, tensors):
-    """:func:`_need` for calls whose own time is a few microseconds: (tensor or None, name,
-    shape, dtype or None for ``dtype``), all on CUDA device ``index``.  What is wrong is said
-    by :func:`_need`."""
-    for t, name, shape, dt in tensors:
-        if t is not None and not (t.shape == shape and t.dtype is (dt or dtype) and t.is_contiguous()
-                                  and t.get_device() == index):
-            _need(t, name, shape, dt or dtype, torch.device("cuda", index))
+def _fits(t, shape, dtype, index) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -626,14 +621,25 @@ def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, backward=False) ->
 
 def _need_la(q, k, v, log_decay, where, *more):
     """What the linear-attention calls check of their inputs; q's shape tells B, T and H.
-    ``more``: further rows of :func:`_need_all`."""
-    if q.device.type != "cuda":
+    ``more``: further (tensor or None, name, shape, dtype).  The calls take a few
+    microseconds, so what fits is passed over by :func:`_fits` and only the rest goes to
+    :func:`_need`, which says what is wrong."""
+    index, shape, dt = q.get_device(), q.shape, q.dtype
+    if index < 0:
         _on_cuda(q.device, where)
-    code = _dtype_code(q)
-    lead = q.shape[:-1]
-    _need_all(q.get_device(), q.dtype, ((q, "q", q.shape, None), (k, "k", q.shape, None),
-                                        (v, "v", lead + v.shape[-1:], None),
-                                        (log_decay, "log_decay", q.shape[-2:-1], torch.float32)) + more)
+    code = _CODES.get(dt)
+    if code is None:
+        code = _dtype_code(q)
+    lead = shape[:-1]
+    if not (q.is_contiguous() and _fits(k, shape, dt, index) and _fits(v, lead + v.shape[-1:], dt, index)
+            and (log_decay is None or _fits(log_decay, shape[-2:-1], torch.float32, index))):
+        for t, name, want, d in ((q, "q", shape, dt), (k, "k", shape, dt), (v, "v", lead + v.shape[-1:], dt),
+                                 (log_decay, "log_decay", shape[-2:-1], torch.float32)):
+            if t is not None:
+                _need(t, name, want, d, q.device)
+    for t, name, want, d in more:
+        if t is not None and not _fits(t, want, d, index):
+            _need(t, name, want, d, q.device)
     return code
 
 
@@ -654,7 +660,7 @@ def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=
     dv = v.shape[-1]
     state = (B, H, dk, dv)
     code = _need_la(q, k, v, log_decay, "kda_la_forward", (initial_state, "initial_state", state, torch.float32),
-                    (out, "out", (B, T, H, dv), None), (final_state, "final_state", state, torch.float32))
+                    (out, "out", (B, T, H, dv), q.dtype), (final_state, "final_state", state, torch.float32))
     if out is None:
         out = torch.empty_like(v)
     if final_state is None and return_final_state:
@@ -680,7 +686,7 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     state = (B, H, dk, dv)
-    code = _need_la(q, k, v, log_decay, "kda_la_backward", (grad_out, "grad_out", (B, T, H, dv), None),
+    code = _need_la(q, k, v, log_decay, "kda_la_backward", (grad_out, "grad_out", (B, T, H, dv), q.dtype),
                     (initial_state, "initial_state", state, torch.float32),
                     (grad_final_state, "grad_final_state", state, torch.float32))
     dq, dkey, dval = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -696,8 +702,8 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
 
 class LAFunction(torch.autograd.Function):
     """``out, final_state = LAFunction.apply(q, k, v, log_decay, initial_state)`` with
-    ``kda_la_forward`` forward and ``kda_la_backward`` backward.  ``log_decay`` is a
-    constant of the layer: it must not require a gradient."""
+    ``kda_la_forward`` forward and ``kda_la_backward`` backward (once: no gradient of the
+    gradient).  ``log_decay`` is a constant of the layer: it must not require a gradient."""
 
     @staticmethod
     def forward(ctx, q, k, v, log_decay, initial_state):
@@ -708,6 +714,7 @@ class LAFunction(torch.autograd.Function):
         return out, final_state
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out, grad_final_state):
         q, k, v, log_decay, initial_state = ctx.saved_tensors
         g = la_backward(q, k, v, log_decay, grad_out.contiguous(), initial_state,
@@ -727,7 +734,7 @@ def la_decode_step(q, k, v, log_decay, state, *, out=None, scale: float = 0.0):
     B, H, dk = q.shape
     dv = v.shape[-1]
     code = _need_la(q, k, v, log_decay, "kda_la_decode_step", (state, "state", (B, H, dk, dv), torch.float32),
-                    (out, "out", (B, H, dv), None))
+                    (out, "out", (B, H, dv), q.dtype))
     if out is None:
         out = torch.empty_like(v)
     st = _launch(q.get_device(), lib.kda_la_decode_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
@@ -763,13 +770,14 @@ def paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths, *, out=No
         _on_cuda(q.device, "kda_paged_decode_step")
     if (k is None) != (v is None):
         raise ValueError("kda_paged_decode_step: k and v are given together or not at all")
-    code = _dtype_code(q)
+    index, dt, code = q.get_device(), q.dtype, _dtype_code(q)
     cache = (num_pages, page_size, Hkv, D)
-    _need_all(q.get_device(), q.dtype,
-              ((q, "q", q.shape, None), (k, "k", (B, Hkv, D), None), (v, "v", (B, Hkv, D), None),
-               (k_cache, "k_cache", cache, None), (v_cache, "v_cache", cache, None),
-               (block_table, "block_table", (B, max_pages), torch.int32), (lengths, "lengths", (B,), torch.int32),
-               (out, "out", (B, H, D), None)))
+    for t, name, want, d in ((q, "q", (B, H, D), dt), (k, "k", (B, Hkv, D), dt), (v, "v", (B, Hkv, D), dt),
+                             (k_cache, "k_cache", cache, dt), (v_cache, "v_cache", cache, dt),
+                             (block_table, "block_table", (B, max_pages), torch.int32),
+                             (lengths, "lengths", (B,), torch.int32), (out, "out", (B, H, D), dt)):
+        if t is not None and not _fits(t, want, d, index):
+            _need(t, name, want, d, q.device)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:

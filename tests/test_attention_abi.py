@@ -94,9 +94,12 @@ def test_workspace_sizes(lib):
     state = 128 * 128 * 4
     assert fwd(1, 1, 32, 128, 128) == 0                           # one chunk: nothing to cut
     assert fwd(4, 1 << 16, 148, 128, 128) == 0                    # heads fill the device
+    # few heads: many segments, a state for each (and for bf16 what the segments wait on)
+    n = fwd(1, 65536, 4, 128, 128, dtype=torch.float32)
+    assert n % (4 * state) == 0 and n // (4 * state) > 8
     n = fwd(1, 65536, 4, 128, 128)
-    assert n % (4 * state) == 0 and n // (4 * state) > 8          # few heads: many segments
-    assert fwd(1, 65536, 4, 128, 128, backward=True) % (3 * 4 * state) == 0
+    assert n % 256 == 0 and n // (4 * state) > 8
+    assert fwd(1, 65536, 4, 128, 128, dtype=torch.float32, backward=True) % (3 * 4 * state) == 0
     assert fwd(0, 8, 2, 128, 128) == 0 and fwd(1, 8, 2, 96, 128) == 0 and fwd(1, 0, 2, 128, 128) == 0
     paged = kda.paged_decode_workspace_bytes
     assert paged(32, 8, 128) > 0 and paged(7, 2, 128) == 0 and paged(8, 2, 96) == 0
@@ -124,3 +127,32 @@ def test_log_decay_takes_no_gradient(lib):
     q = _host(1, 8, 2, 128)
     with pytest.raises(ValueError, match="constant"):
         kda.LAFunction.apply(q, q, q, torch.zeros(2, requires_grad=True), None)
+
+
+def test_the_split_of_the_units_and_its_inverse():
+    # paged rows: owner c of G has the units [c U / G, (c + 1) U / G); the joining kernel finds the
+    # owner of unit x as ((x + 1) G - 1) / U.  Every owner has a unit, and the two agree.
+    import random
+    rng = random.Random(3)
+    for _ in range(300):
+        units, grid = rng.randint(1, 5000), rng.choice((1, 148, 296, 592))
+        owners = min(units, grid)
+        starts = [c * units // owners for c in range(owners + 1)]
+        assert starts[0] == 0 and starts[-1] == units and all(a < b for a, b in zip(starts, starts[1:]))
+        assert max(b - a for a, b in zip(starts, starts[1:])) - min(b - a for a, b in zip(starts, starts[1:])) <= 1
+        for x in {0, units - 1} | {rng.randrange(units) for _ in range(20)}:
+            c = ((x + 1) * owners - 1) // units
+            assert starts[c] <= x < starts[c + 1]
+
+
+def test_division_by_the_page_size():
+    # the quotient t / d as (floor(m t / 2^32) + t) / 2^l, for every page size and position allowed
+    import random
+    rng = random.Random(4)
+    for _ in range(20000):
+        d = rng.choice((rng.randint(1, 300), rng.randint(1, 2 ** 31 - 1025), 1 << rng.randint(0, 30)))
+        t = rng.choice((rng.randint(0, 2 ** 31 - 1), rng.randint(0, 5000), min(2 ** 31 - 1, max(0, d * rng.randint(0, 9) + rng.randint(-1, 1)))))
+        l = (d - 1).bit_length()
+        m = ((1 << 32) * ((1 << l) - d)) // d + 1
+        high = (m * t) >> 32
+        assert m < 1 << 32 and high + t < 1 << 32 and (high + t) >> l == t // d

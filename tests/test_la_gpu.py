@@ -298,3 +298,36 @@ def test_gradients_are_the_slopes_of_differences():
         want = float((g[gn].double() * step.double()).sum())
         size = float(g[gn].double().norm() * step.double().norm())
         assert abs(slope - want) <= 1e-5 * size, n
+
+
+def test_refusals_of_the_binding():
+    x = _inputs(1, 20, 3, 128, 128, "bf16", 30)
+    call = lambda **kw: _forward(dict(x, **kw))
+    with pytest.raises(ValueError, match="contiguous"):
+        call(k=x["k"].transpose(1, 2).contiguous().transpose(1, 2))
+    with pytest.raises(ValueError, match="shape"):
+        call(k=x["k"][:, :19].contiguous())
+    with pytest.raises(ValueError, match="log_decay"):
+        call(log_decay=x["log_decay"][:2].contiguous())
+    with pytest.raises(TypeError, match="v must be"):
+        call(v=x["v"].float())
+    with pytest.raises(TypeError):
+        call(q=x["q"].half(), k=x["k"].half(), v=x["v"].half())
+    with pytest.raises(ValueError, match="initial_state is on"):
+        call(state=x["state"].cpu())
+    with pytest.raises(TypeError, match="out must be"):
+        _forward(x, out=torch.empty(x["v"].shape, device="cuda"))
+    with pytest.raises(kda.KDAError, match="MISALIGNED"):
+        room = torch.empty(x["q"].numel() + 1, dtype=torch.bfloat16, device="cuda")
+        call(q=room[1:].view(x["q"].shape))
+    with pytest.raises(kda.KDAError, match="UNSUPPORTED"):
+        _forward({n: (t[..., :96].contiguous() if n in ("q", "k") else None if n in ("state", "gs") else t) for n, t in x.items()})
+
+
+def test_no_second_derivative():
+    x = _inputs(1, 20, 2, 64, 64, "f32", 31, state=False)
+    q = x["q"].requires_grad_(True)
+    out, _ = kda.LAFunction.apply(q, x["k"], x["v"], x["log_decay"], None)
+    (g,) = torch.autograd.grad(out.square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
