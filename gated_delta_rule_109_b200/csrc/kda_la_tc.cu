@@ -67,8 +67,8 @@ constexpr uint32_t SM_BAR = SM_LC + 16;
 constexpr int kKpSlots = 5;
 enum Bar {
     FULL_Q = 0, FULL_K = 2, FULL_V = 4, FREE_K = 6, FREE_V = 8, OUT_READY = 10, U_READY = 12, U_FREE = 14,
-    KP_READY = 16, KP_FREE = KP_READY + kKpSlots, S_READY = KP_FREE + kKpSlots, QS_READY, PV_GO, PV_DONE,
-    O_FREE, S0_READY, kBars
+    X_FULL = 16, X_FREE = 18, KP_READY = 20, KP_FREE = KP_READY + kKpSlots, S_READY = KP_FREE + kKpSlots, QS_READY,
+    PV_GO, PV_DONE, O_FREE, S0_READY, kBars
 };
 constexpr uint32_t SM_TMEM = SM_BAR + 8 * kBars;      // address of the tensor memory, work item
 constexpr uint32_t SM_TOTAL = SM_TMEM + 16;
@@ -232,13 +232,6 @@ __device__ __forceinline__ int load_acquire(const int *p)
     asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ float4 load_l2(const float4 *p)
-{
-    float4 v;
-    asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
-    return v;
-}
-
 // ---- the state of work item x, 64 floats a thread: key channel r, value columns 64 part ..
 __device__ __forceinline__ int reread(uint32_t saddr)
 {
@@ -305,55 +298,19 @@ __device__ __forceinline__ void store_final(const LaArgs &a, int x, int r, int p
 #pragma unroll
     for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
 }
-// S to state `g` of the workspace's chain of item x: 16 x float4 of thread `me`, a warp's 512
-// bytes beside each other; `tell`: counted for those that wait for it.
-__device__ __forceinline__ void leave_state(const LaArgs &a, int x, int g, int me, bool tell, int *flags, float *slots,
+// S to state `g` of the workspace's chain of item x, 16 x float4 of thread `me`, a warp's 512
+// bytes beside each other, and counted for those that wait for it.
+__device__ __forceinline__ void leave_state(const LaArgs &a, int x, int g, int me, int *flags, float *slots,
                                             const float (&S)[64])
 {
     const size_t at = (size_t)(x % (a.npass * a.B * a.H)) * a.nseg + g;
     float4 *dst = reinterpret_cast<float4 *>(slots + at * kSlotFloats) + me;
 #pragma unroll
     for (int i = 0; i < 16; ++i) dst[256 * i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    if (tell) {
-        __threadfence();
-        __syncwarp();
-        if ((me & 31) == 0) atomicAdd(flags + 1 + at, 1);
-    }
+    __threadfence();
+    __syncwarp();
+    if ((me & 31) == 0) atomicAdd(flags + 1 + at, 1);
 }
-// The state that enters the segment, whatever S held: the contributions of all segments before
-// it, or what segment 0 started from.  False if one did not come.
-__device__ __forceinline__ bool entering_state(const LaArgs &a, int x, int me, const int *flags, const float *slots,
-                                               float (&S)[64])
-{
-    const int heads = a.npass * a.B * a.H, seg = x / heads;
-    const size_t chain = (size_t)(x % heads) * a.nseg;
-    int bh;
-    const LaPass &ps = pass_of(a, x, bh);
-    for (int g = 0; g < max(seg, 1); ++g) {
-        const size_t at = chain + (seg == 0 ? a.nseg - 1 : g);
-        const long long t0 = clock64();
-        while (seg > 0 && !__all_sync(0xffffffffu, load_acquire(flags + 1 + at) == kStateWarps))
-            if (__any_sync(0xffffffffu, clock64() - t0 > kWaitCycles)) {
-                atomicOr(&g_la_device_status, 1u);
-                return false;
-            }
-        int t0g, t1g;
-        la_segment(g, a.nseg, a.seg_tokens, a.T, ps.rev, t0g, t1g);
-        const double l = g == 0 ? 0.0 : la_power(a.log_decay, bh % a.H, t1g - t0g);
-        const float lh = (float)l, ll = (float)(l - (double)lh);
-        const float4 *src = reinterpret_cast<const float4 *>(slots + at * kSlotFloats) + me;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float4 w = load_l2(src + 256 * i);
-            S[4 * i] = fmaf(lh, S[4 * i], fmaf(ll, S[4 * i], w.x));
-            S[4 * i + 1] = fmaf(lh, S[4 * i + 1], fmaf(ll, S[4 * i + 1], w.y));
-            S[4 * i + 2] = fmaf(lh, S[4 * i + 2], fmaf(ll, S[4 * i + 2], w.z));
-            S[4 * i + 3] = fmaf(lh, S[4 * i + 3], fmaf(ll, S[4 * i + 3], w.w));
-        }
-    }
-    return true;
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
 la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps maps, int *flags, float *slots)
 {
@@ -371,7 +328,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                               : (i >= OUT_READY && i < U_READY) || i == O_FREE ? kRowWarps
                               : i == PV_GO ? 2 * kRowWarps
                               : (i >= KP_READY && i < KP_FREE) ? kKeyWarps / 2
-                              : (i >= U_FREE && i < KP_READY) || i == S0_READY ? kStateWarps : 1;
+                              : (i >= U_FREE && i < X_FULL) || (i >= X_FREE && i < KP_READY) || i == S0_READY ? kStateWarps : 1;
             mbar_init(bar(i), (uint32_t)count);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -404,7 +361,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 const int t = chunk_at(it < nown ? it : it - nown) * kC;
                 load_tile(&maps.k[ip], sb + SM_K + it * kTile, bar(FULL_K + it), h, t, b);
                 load_tile(&maps.v[ip], sb + SM_V + it * kTile, bar(FULL_V + it), h, t, b);
-                if (it >= nown) load_tile(&maps.q[ip], sb + SM_Q + (it - nown) * kTile, bar(FULL_Q + it - nown), h, t, b);
+                if (a.nseg == 1) load_tile(&maps.q[ip], sb + SM_Q + it * kTile, bar(FULL_Q + it), h, t, b);
             }
         __syncwarp();
     } else if (tid < 256) {
@@ -624,14 +581,42 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         };
         if (a.nseg > 1) {
             const int me = tid - 32 * kStateWarp0;
-            if (seg == 0) leave_state(a, reread(sb + SM_TMEM + 4), a.nseg - 1, me, false, flags, slots, S);
+            if (seg == 0) leave_state(a, reread(sb + SM_TMEM + 4), a.nseg - 1, me, flags, slots, S);
             const int three_own = three_from(ps.sT);
             for (int j = 0; j < nown; ++j)
                 if (!absorb(j & 1, j >> 1, j, j >= three_own)) break;
             if (ok) {
                 const int x0 = reread(sb + SM_TMEM + 4);
-                if (nown > 0) leave_state(a, x0, x0 / heads, me, true, flags, slots, S);
-                ok = entering_state(a, x0, me, flags, slots, S);
+                if (nown > 0) leave_state(a, x0, x0 / heads, me, flags, slots, S);
+                // The state that enters the segment: the contributions of all segments before it, or
+                // what segment 0 started from, one after the other through the q tiles.  Lane g holds
+                // how much fades over segment g.
+                float wh = 0.f, wl = 0.f;
+                if (lane > 0 && lane < x0 / heads) {
+                    int bh0, t0, t1;
+                    const LaPass &p0 = pass_of(a, x0, bh0);
+                    la_segment(lane, a.nseg, a.seg_tokens, a.T, p0.rev, t0, t1);
+                    const double l = la_power(a.log_decay, bh0 % a.H, t1 - t0);
+                    wh = (float)l;
+                    wl = (float)(l - (double)wh);
+                }
+                for (int g = 0; ok && g < max(x0 / heads, 1); ++g) {
+                    const float lh = __shfl_sync(0xffffffffu, wh, g), ll = __shfl_sync(0xffffffffu, wl, g);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (!wait_warp(X_FULL + half, g)) break;
+                        const uint32_t src = sb + SM_Q + (uint32_t)(half * kTile + 16 * me);
+#pragma unroll
+                        for (int i = 32 * half; i < 32 * half + 32; i += 4) {
+                            float u[4];
+                            asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3])
+                                         : "r"(src + (uint32_t)(1024 * (i - 32 * half))) : "memory");
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) S[i + y] = fmaf(lh, S[i + y], fmaf(ll, S[i + y], u[y]));
+                        }
+                        arrive_warp(X_FREE + half);
+                    }
+                }
             }
         }
         if (ok) publish();
@@ -653,6 +638,33 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 tma_store_4d(&maps.out[ip], src + kHalf, 64, h, t, b);
                 bulk_commit();
             };
+            auto load_q = [&](int j) {
+                load_tile(&maps.q[ip], sb + SM_Q + (j & 1) * kTile, bar(FULL_Q + (j & 1)), h, chunk_at(j) * kC, b);
+            };
+            // the states that enter the segment's outputs, in halves of 32 KB through the q tiles
+            int halves = 0;
+            auto load_states = [&] {
+                const size_t chain = (size_t)(item % heads) * a.nseg;
+                for (int g = 0; g < max(seg, 1); ++g) {
+                    const size_t at = chain + (seg == 0 ? a.nseg - 1 : g);
+                    const long long t0 = clock64();
+                    while (load_acquire(flags + 1 + at) != kStateWarps)
+                        if (clock64() - t0 > kWaitCycles) {
+                            ok = false;
+                            atomicOr(&g_la_device_status, 1u);
+                            return;
+                        }
+                    asm volatile("fence.proxy.async;" ::: "memory");        // plain stores there, bulk copies here
+                    for (int half = 0; half < 2; ++half) {
+                        if (g > 0 && !wait(X_FREE + half, g - 1)) return;
+                        mbar_expect_tx(bar(X_FULL + half), kTile);
+                        bulk_g2s(sb + SM_Q + half * kTile, reinterpret_cast<const uint8_t *>(slots + at * kSlotFloats) + half * kTile,
+                                 kTile, bar(X_FULL + half));
+                        ++halves;
+                    }
+                }
+                for (int half = 0; half < 2; ++half) wait(X_FREE + half, max(seg, 1) - 1);
+            };
             int it = 0;
             for (; it < nsteps; ++it) {
                 const int st = it & 1, j = it < nown ? it : it - nown, t = chunk_at(j) * kC;
@@ -662,14 +674,17 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     if (!wait(FREE_V + st, (it >> 1) - 1)) break;
                     load_tile(&maps.v[ip], sb + SM_V + st * kTile, bar(FULL_V + st), h, t, b);
                 }
-                if (it >= nown && (it >= 2 || nown > 0)) {
-                    if (j >= 2) {
-                        // the outputs of chunk j - 2 leave the q tile, then it is loaded again
-                        if (!wait(OUT_READY + (j & 1), (j >> 1) - 1)) break;
-                        store(j - 2);
-                        bulk_wait_read();
-                    }
-                    if (it >= 2) load_tile(&maps.q[ip], sb + SM_Q + (j & 1) * kTile, bar(FULL_Q + (j & 1)), h, t, b);
+                if (it < nown) continue;
+                if (j >= 2) {
+                    // the outputs of chunk j - 2 leave the q tile, then it is loaded again
+                    if (!wait(OUT_READY + (j & 1), (j >> 1) - 1)) break;
+                    store(j - 2);
+                    bulk_wait_read();
+                    load_q(j);
+                } else if (a.nseg > 1 && (j == 1 || nchunks == 1)) {
+                    load_states();
+                    if (!ok) break;
+                    for (int x = 0; x <= j; ++x) load_q(x);
                 }
             }
             for (int j = max(nchunks - 2, 0); j < nchunks && ok; ++j) {
@@ -683,6 +698,8 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                     mbar_wait(bar(FULL_V + (i & 1)), (i >> 1) & 1);
                     if (i >= nown) mbar_wait(bar(FULL_Q + ((i - nown) & 1)), ((i - nown) >> 1) & 1);
                 }
+            if (!ok)
+                for (int x = max(halves - 2, 0); x < halves; ++x) mbar_wait(bar(X_FULL + (x & 1)), (x >> 1) & 1);
         }
     } else if (warp == kMmaWarp) {
         // Whole warps walk the loops and one elected lane issues, so that descriptors stay in
