@@ -316,7 +316,8 @@ cudaError_t launch_typed(const LaArgs &a, cudaStream_t stream)
 template <typename InT, bool STATES_ONLY>
 cudaError_t launch_dims(const LaArgs &a, cudaStream_t stream)
 {
-    if (a.dk == 128 && a.dv == 128) return launch_typed<128, 128, InT, STATES_ONLY>(a, stream);
+    if constexpr (sizeof(InT) == 4)             // bf16 runs on the tensor cores there
+        if (a.dk == 128 && a.dv == 128) return launch_typed<128, 128, InT, STATES_ONLY>(a, stream);
     if (a.dk == 64 && a.dv == 64) return launch_typed<64, 64, InT, STATES_ONLY>(a, stream);
     if (a.dk == 128 && a.dv == 64) return launch_typed<128, 64, InT, STATES_ONLY>(a, stream);
     if (a.dk == 64 && a.dv == 128) return launch_typed<64, 128, InT, STATES_ONLY>(a, stream);

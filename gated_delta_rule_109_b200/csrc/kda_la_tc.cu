@@ -239,11 +239,13 @@ __device__ __forceinline__ int reread(uint32_t saddr)
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(saddr) : "memory");
     return v;
 }
+// Work items: segments outermost, then heads, then passes, so that the passes of a head, which
+// read the same four tensors, run beside each other and find them in L2.
 __device__ __forceinline__ const LaPass &pass_of(const LaArgs &a, int x, int &bh)
 {
-    const int heads = a.B * a.H;
-    bh = x % heads;
-    return a.pass[x / heads % a.npass];
+    const int chain = x % (a.npass * a.B * a.H);
+    bh = chain / a.npass;
+    return a.pass[chain % a.npass];
 }
 // The pass's initial state, or zeros (`zero`, or none given).  32 rows x 32 columns at a time go
 // through 4 KB of shared memory of the warp's own, so that global memory is read by whole
@@ -342,7 +344,7 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
     __syncthreads();
     tc_fence_after();
     const int item = *reinterpret_cast<const int *>(smem + SM_TMEM + 4);
-    const int seg = item / heads, ip = item % heads / (a.B * a.H), bh = item % (a.B * a.H);
+    const int seg = item / heads, ip = item % heads % a.npass, bh = item % heads / a.npass;
     const LaPass &ps = a.pass[ip];
     const int b = bh / a.H, h = bh % a.H, rev = ps.rev;
     int t_lo, t_hi;
