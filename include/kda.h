@@ -567,8 +567,10 @@ kda_status kda_la_decode_step(const void *q, const void *k, const void *v, const
  *                 to be used by another call that may run at the same time
  *
  * A row with lengths[b] < 0 is idle: its cache and its row of out are left as they were.  A
- * row without keys (k = v = NULL, lengths[b] = 0) gets zeros.  Rows may share pages that
- * they only read; two rows that write the same position leave one of the two there.
+ * row without keys (k = v = NULL, lengths[b] = 0) gets zeros.  Rows may share pages; each
+ * attends to its own new key, which is taken from k and v.  The position that a row writes
+ * must not be one that another row reads from the cache (t < lengths[b]); where two rows
+ * write the same position, it holds elements of either afterwards.
  * Memory of the cache behind a row's last key is never used, whatever it holds.  Lengths
  * and pages are read on the device.  A page outside [0, num_pages) counts as absent (its
  * keys weigh nothing, a key for it is not stored), a row longer than its table is left as

@@ -168,6 +168,59 @@ def test_in_place_state_of_a_cut_sequence():
     assert torch.equal(out, out2) and torch.equal(last, state)
 
 
+@pytest.mark.parametrize("dtype,B,T,H,at", [("bf16", 1, 65517, 32, 8191), ("bf16", 3, 9001, 61, 2063),
+                                            ("f32", 1, 20011, 20, 3001)])
+def test_a_long_call_equals_its_pieces(dtype, B, T, H, at):
+    """More work items than the GPU has places for at once, against the same sequence in pieces
+    that carry the state (and, backwards, its gradient).  Each side is within the tolerances at
+    the top of the reference, so the two are within their sum, head by head."""
+    x = _inputs(B, T, H, 128, 128, dtype, 21)
+    out, last = _forward(x)
+    g = _backward(x)
+    pieces = [slice(t, min(t + at, T)) for t in range(0, T, at)]
+    cut = lambda s: {n: x[n][:, s].contiguous() for n in ("q", "k", "v", "go")}
+    states, state = [], x["state"]
+    for s in pieces:
+        states.append(state)
+        o, state = _forward(dict(x, **cut(s), state=state))
+        _same_heads(out[:, s], o, dtype, 2)
+    _same_heads(last[:, None], state[:, None], "f32", 3)
+    gs = x["gs"]
+    for s, state in zip(reversed(pieces), reversed(states)):
+        p = _backward(dict(x, **cut(s), state=state, gs=gs))
+        gs = p["dinitial_state"]
+        for n in ("dq", "dk", "dv"):
+            _same_heads(g[n][:, s], p[n], dtype, 2)
+    _same_heads(g["dinitial_state"][:, None], gs[:, None], "f32", 3)
+
+
+def _same_heads(a, b, dtype, head_axis):
+    tol = 4 * HALF if dtype == "bf16" else 4e-5
+    if head_axis == 3:                      # states [B, 1, H, dk, dv]
+        a, b = a.flatten(3), b.flatten(3)
+    a, b = (y.transpose(1, 2).flatten(2).double() for y in (a, b))      # [B, H, all of a head]
+    assert bool(torch.isfinite(a).all())
+    assert bool(((a - b).norm(dim=-1) <= tol * b.norm(dim=-1) + 1e-30).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("length", [0, 1, 100, 128, 300])
+def test_a_sequence_padded_with_zeros(dtype, length):
+    x = _inputs(2, 389, 6, 128, 128, dtype, 22)
+    for n in ("q", "k", "v", "go"):
+        x[n][0, length:] = 0
+    out, last = _forward(x)
+    g = _backward(x)
+    assert not out[0, length:].any() and not any(g[n][0, length:].any() for n in ("dq", "dk", "dv"))
+    _check_forward(x, out, last)
+    _check_backward(x, g)
+    short = {n: x[n][:1, :length].contiguous() for n in ("q", "k", "v")}
+    y = dict(x, **short, state=x["state"][:1].contiguous(), log_decay=None)
+    _, at_end = _forward(y)
+    _, padded = _forward(dict(x, log_decay=None))
+    assert float((at_end - padded[:1]).norm()) <= 2e-5 * float(at_end.norm())
+
+
 def test_no_tokens():
     x = _inputs(2, 0, 3, 128, 128, "bf16", 12)
     out, last = _forward(x)

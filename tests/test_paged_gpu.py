@@ -147,6 +147,27 @@ def test_rows_share_pages():
     _run(x)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [0, 31, 64, 700])
+def test_rows_that_write_one_position_attend_to_their_own_key(n, dtype):
+    x = _case([n, n], 8, 2, 128, 16, dtype, 17, hostile=False)
+    x["block_table"][1] = x["block_table"][0]
+    before = x["k_cache"].clone(), x["v_cache"].clone()
+    out = _call(x)
+    kda.check_status()
+    for b in range(2):
+        y = dict(x, q=x["q"][b:b + 1], k=x["k"][b:b + 1], v=x["v"][b:b + 1], block_table=x["block_table"][b:b + 1],
+                 lengths=x["lengths"][b:b + 1], k_cache=before[0].clone(), v_cache=before[1].clone())
+        alone = _call({m: t.contiguous() for m, t in y.items()})
+        assert torch.allclose(out[b:b + 1].float(), alone.float(), rtol=2 * HALF if dtype == "bf16" else 1e-4,
+                              atol=2 * HALF if dtype == "bf16" else 1e-4)
+    for c, old, new in ((x["k_cache"], before[0], x["k"]), (x["v_cache"], before[1], x["v"])):
+        page, row = int(x["block_table"][0, n // 16]), n % 16
+        assert bool(((c[page, row] == new[0]) | (c[page, row] == new[1])).all())
+        c[page, row] = old[page, row]
+        assert torch.equal(c, old)
+
+
 def test_a_run_of_steps_fills_the_cache():
     x = _case([14, -1, 0, 62], 8, 4, 128, 16, "bf16", 12, spare=12)
     every = torch.arange(x["k_cache"].shape[0], device="cuda", dtype=torch.int32)
