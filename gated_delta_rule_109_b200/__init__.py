@@ -588,7 +588,7 @@ def gdn_decode_step(q, k, v, log_alpha, beta, state, *, out=None, scale: float =
 
 def _launch(index: int, fn, *args) -> int:
     """fn(*args, current stream) with the tensors' device as the current one."""
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         return fn(*args, _raw_stream(index))
     with torch.cuda.device(index):
         return fn(*args, _raw_stream(index))
@@ -630,11 +630,13 @@ def _need_la(q, k, v, log_decay, where, *more):
     code = _CODES.get(dt)
     if code is None:
         code = _dtype_code(q)
-    lead = shape[:-1]
-    if not (q.is_contiguous() and _fits(k, shape, dt, index) and _fits(v, lead + v.shape[-1:], dt, index)
-            and (log_decay is None or _fits(log_decay, shape[-2:-1], torch.float32, index))):
-        for t, name, want, d in ((q, "q", shape, dt), (k, "k", shape, dt), (v, "v", lead + v.shape[-1:], dt),
-                                 (log_decay, "log_decay", shape[-2:-1], torch.float32)):
+    vshape = v.shape
+    if vshape != shape:                     # dv may differ
+        vshape = shape[:-1] + vshape[-1:]
+    if not (q.is_contiguous() and _fits(k, shape, dt, index) and _fits(v, vshape, dt, index)
+            and (log_decay is None or _fits(log_decay, (shape[-2],), torch.float32, index))):
+        for t, name, want, d in ((q, "q", shape, dt), (k, "k", shape, dt), (v, "v", vshape, dt),
+                                 (log_decay, "log_decay", (shape[-2],), torch.float32)):
             if t is not None:
                 _need(t, name, want, d, q.device)
     for t, name, want, d in more:
@@ -664,7 +666,7 @@ def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=
     if out is None:
         out = torch.empty_like(v)
     if final_state is None and return_final_state:
-        final_state = q.new_empty(state, dtype=torch.float32)
+        final_state = q.new_empty(state, dtype=torch.float32) if initial_state is None else torch.empty_like(initial_state)
     ws, nbytes, _hold = _la_workspace(lib.kda_la_forward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_forward")
     st = _launch(q.get_device(), lib.kda_la_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
                  _address(initial_state), out.data_ptr(), _address(final_state), B, T, H, dk, dv, code, scale, ws, nbytes)
