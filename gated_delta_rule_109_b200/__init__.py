@@ -19,6 +19,7 @@ library is not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -598,12 +599,18 @@ def _address(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-def _la_workspace(fn, q, dk, dv, code, workspace, where):
+@functools.lru_cache(maxsize=256)
+def _size(name, *sizes) -> int:
+    """A workspace's bytes from the library, which depend on nothing but these sizes."""
+    return getattr(load(), name)(*sizes)
+
+
+def _la_workspace(q, dk, dv, code, workspace, where):
     """Address and bytes of a linear-attention call's workspace, and the tensor: the caller's,
     or a new one where the sizes need any (from torch's allocator, on the current stream)."""
     B, T, H = q.shape[:3]
     if workspace is None:
-        n = fn(B, T, H, dk, dv, code)
+        n = _size(where + "_workspace_bytes", B, T, H, dk, dv, code)
         if not n:
             return None, 0, None
         workspace = q.new_empty(n, dtype=torch.uint8)
@@ -667,7 +674,7 @@ def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=
         out = torch.empty_like(v)
     if final_state is None and return_final_state:
         final_state = q.new_empty(state, dtype=torch.float32) if initial_state is None else torch.empty_like(initial_state)
-    ws, nbytes, _hold = _la_workspace(lib.kda_la_forward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_forward")
+    ws, nbytes, _hold = _la_workspace(q, dk, dv, code, workspace, "kda_la_forward")
     st = _launch(q.get_device(), lib.kda_la_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
                  _address(initial_state), out.data_ptr(), _address(final_state), B, T, H, dk, dv, code, scale, ws, nbytes)
     if st:
@@ -693,7 +700,7 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
                     (grad_final_state, "grad_final_state", state, torch.float32))
     dq, dkey, dval = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds0 = q.new_empty(state, dtype=torch.float32) if initial_state_grad else None
-    ws, nbytes, _hold = _la_workspace(lib.kda_la_backward_workspace_bytes, q, dk, dv, code, workspace, "kda_la_backward")
+    ws, nbytes, _hold = _la_workspace(q, dk, dv, code, workspace, "kda_la_backward")
     st = _launch(q.get_device(), lib.kda_la_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
                  _address(initial_state), grad_out.data_ptr(), _address(grad_final_state), dq.data_ptr(),
                  dkey.data_ptr(), dval.data_ptr(), _address(ds0), B, T, H, dk, dv, code, scale, ws, nbytes)
@@ -768,27 +775,34 @@ def paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths, *, out=No
     B, H, D = q.shape
     num_pages, page_size, Hkv = k_cache.shape[:3]
     max_pages = block_table.shape[-1]
-    if q.device.type != "cuda":
+    index, dt = q.get_device(), q.dtype
+    if index < 0:
         _on_cuda(q.device, "kda_paged_decode_step")
     if (k is None) != (v is None):
         raise ValueError("kda_paged_decode_step: k and v are given together or not at all")
-    index, dt, code = q.get_device(), q.dtype, _dtype_code(q)
-    cache = (num_pages, page_size, Hkv, D)
-    for t, name, want, d in ((q, "q", (B, H, D), dt), (k, "k", (B, Hkv, D), dt), (v, "v", (B, Hkv, D), dt),
-                             (k_cache, "k_cache", cache, dt), (v_cache, "v_cache", cache, dt),
-                             (block_table, "block_table", (B, max_pages), torch.int32),
-                             (lengths, "lengths", (B,), torch.int32), (out, "out", (B, H, D), dt)):
-        if t is not None and not _fits(t, want, d, index):
-            _need(t, name, want, d, q.device)
+    code = _CODES.get(dt)
+    if code is None:
+        code = _dtype_code(q)
+    cache, new = (num_pages, page_size, Hkv, D), (B, Hkv, D)
+    if not (q.is_contiguous() and (k is None or _fits(k, new, dt, index) and _fits(v, new, dt, index))
+            and _fits(k_cache, cache, dt, index) and _fits(v_cache, cache, dt, index)
+            and _fits(block_table, (B, max_pages), torch.int32, index) and _fits(lengths, (B,), torch.int32, index)
+            and (out is None or _fits(out, (B, H, D), dt, index))):
+        for t, name, want, d in ((q, "q", (B, H, D), dt), (k, "k", new, dt), (v, "v", new, dt),
+                                 (k_cache, "k_cache", cache, dt), (v_cache, "v_cache", cache, dt),
+                                 (block_table, "block_table", (B, max_pages), torch.int32),
+                                 (lengths, "lengths", (B,), torch.int32), (out, "out", (B, H, D), dt)):
+            if t is not None:
+                _need(t, name, want, d, q.device)
     if out is None:
         out = torch.empty_like(q)
     if workspace is None:
-        nbytes = lib.kda_paged_decode_workspace_bytes(H, Hkv, D, code)
+        nbytes = _size("kda_paged_decode_workspace_bytes", H, Hkv, D, code)
         workspace = q.new_empty(nbytes, dtype=torch.uint8)
     else:
         _need_workspace(workspace, q.device, "kda_paged_decode_step")
         nbytes = workspace.numel() * workspace.element_size()
-    st = _launch(q.get_device(), lib.kda_paged_decode_step, q.data_ptr(), _address(k), _address(v), k_cache.data_ptr(),
+    st = _launch(index, lib.kda_paged_decode_step, q.data_ptr(), _address(k), _address(v), k_cache.data_ptr(),
                  v_cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), B, H, Hkv, D, num_pages,
                  page_size, max_pages, code, scale, workspace.data_ptr(), nbytes)
     if st:
