@@ -41,27 +41,28 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float acc)
     return acc;
 }
 
-// R rows of D channels, one per token t (zeros from c on), to shared memory as fp32.  The loads
-// are all issued before the first is needed.
+// A chunk's rows of D channels to shared memory as fp32, in the order of the walk: row t is
+// token t (forward) or c - 1 - t (reversed), rows from c on are zeros.  `src` is row 0's, `step`
+// leads to the next.  The loads are all issued before the first is needed.
 template <int D>
-__device__ __forceinline__ void stage(float *dst, const float *src, size_t token_stride, int c, int tid)
+__device__ __forceinline__ void stage(float *dst, const float *src, ptrdiff_t step, int c, int tid)
 {
 #pragma unroll
     for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
         const int id = e * kThreads + tid, t = id / (D / 4), x = 4 * (id % (D / 4));
         const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + t * (D + 4) + x);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                     :: "r"(to), "l"(src + (t < c ? t * token_stride + x : 0)), "r"(t < c ? 16 : 0) : "memory");
+                     :: "r"(to), "l"(src + (t < c ? t * step + x : 0)), "r"(t < c ? 16 : 0) : "memory");
     }
 }
 template <int D>
-__device__ __forceinline__ void stage(float *dst, const __nv_bfloat16 *src, size_t token_stride, int c, int tid)
+__device__ __forceinline__ void stage(float *dst, const __nv_bfloat16 *src, ptrdiff_t step, int c, int tid)
 {
     float4 v[kC * D / 4 / kThreads];
 #pragma unroll
     for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
         const int id = e * kThreads + tid, t = id / (D / 4), x = 4 * (id % (D / 4));
-        v[e] = t < c ? la_load4(src + t * token_stride + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[e] = t < c ? la_load4(src + t * step + x) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
@@ -85,7 +86,12 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
     float *sW = sm + L::off_w;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    // A product's 64 x 64 tile: warp w has rows 16 wr .. and columns 32 wc .., a lane 4 rows and 4
+    // columns of them, so that a warp's 16-byte reads of an operand are 64 or 128 bytes of different
+    // banks.  Warps w and w + 4 share a scheduler: together they have as many causal pairs as any two.
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wr = warp < 4 ? warp : 7 - warp, wc = warp >> 2, ry = lane >> 3, cx = lane & 7;
+    const int row0 = 16 * wr + ry, col4 = 32 * wc + 4 * cx;     // rows row0 + 4 i; channels col4 + 64 m ..
     const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
     const int seg = blockIdx.x % nwork;
     const int bh = (blockIdx.x / nwork) % (a.B * a.H);
@@ -103,6 +109,24 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
         sm[L::off_l + 2 * (tid - 96)] = (float)l;
         sm[L::off_l + 2 * (tid - 96) + 1] = (float)(l - (double)(float)l);
     }
+    const InT *q = static_cast<const InT *>(ps.q), *k = static_cast<const InT *>(ps.k), *v = static_cast<const InT *>(ps.v);
+    const int n0 = t_lo / kC, n1 = (t_hi + kC - 1) / kC;
+    auto tokens_of = [&](int it, int &t0, int &c) {             // the walk's chunk `it`: first token, tokens
+        t0 = (rev ? n1 - 1 - (it - n0) : it) * kC;
+        c = min(kC, t_hi - t0);
+    };
+    // token of row t of chunk `it`, counted over [B, T, H]
+    auto token_at = [&](int t0, int c, int t) { return ((size_t)b * a.T + t0 + (rev ? c - 1 - t : t)) * a.H + h; };
+    auto load = [&](int it) {
+        int t0, c;
+        tokens_of(it, t0, c);
+        const size_t at = token_at(t0, c, 0);
+        const ptrdiff_t step = rev ? -(ptrdiff_t)a.H : (ptrdiff_t)a.H;
+        if (!STATES_ONLY) stage<DK>(sQ, q + at * DK, step * DK, c, tid);
+        stage<DK>(sK, k + at * DK, step * DK, c, tid);
+        stage<DV>(sV, v + at * DV, step * DV, c, tid);
+    };
+    load(n0);                               // under way while the entering state is made
     // ---- entering state.  One segment, and segment 0 of the walk without outputs: the initial
     // state (kept in slot nseg - 1 for the outputs of segment 0: final_state may be the same
     // buffer).  Otherwise the earlier segments' contributions, each faded by the tokens between.
@@ -117,16 +141,26 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
             weight[2 * tid + 1] = (float)(l - (double)(float)l);
         }
         __syncthreads();
-        for (int e = 4 * tid; e < DK * DV; e += 4 * kThreads) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (seg == 0) s = la_load4(slots + (size_t)(a.nseg - 1) * DK * DV + e);
-#pragma unroll 8
-            for (int g = 0; g < seg; ++g) {
-                const float4 u = la_load4(slots + (size_t)g * DK * DV + e);
-                fma4(s, weight[2 * g + 1], u);
-                fma4(s, weight[2 * g], u);
+#pragma unroll 1
+        for (int e0 = 4 * tid; e0 < DK * DV; e0 += 16 * kThreads) {
+            float4 s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s[i] = seg == 0 ? la_load4(slots + (size_t)(a.nseg - 1) * DK * DV + e0 + 4 * i * kThreads)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int g = 0; g < seg; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 u = la_load4(slots + (size_t)g * DK * DV + e0 + 4 * i * kThreads);
+                    fma4(s[i], weight[2 * g + 1], u);
+                    fma4(s[i], weight[2 * g], u);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = e0 + 4 * i * kThreads;
+                la_store4(sS + (e / DV) * PV + e % DV, s[i]);
             }
-            la_store4(sS + (e / DV) * PV + e % DV, s);
         }
     } else {
         const float *s0 = ps.s0 && (!STATES_ONLY || seg == 0) ? ps.s0 + (size_t)bh * DK * DV : nullptr;
@@ -143,59 +177,58 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
         }
     }
 
-    const InT *q = static_cast<const InT *>(ps.q), *k = static_cast<const InT *>(ps.k), *v = static_cast<const InT *>(ps.v);
-    const int n0 = t_lo / kC, n1 = (t_hi + kC - 1) / kC;
     for (int it = n0; it < n1; ++it) {
-        const int n = rev ? n1 - 1 - (it - n0) : it;
-        const int t0 = n * kC, c = min(kC, t_hi - t0);
-        __syncthreads();                        // the chunk before is consumed
-        // ---- stage q, k, v (rows past c are zero: they change nothing)
-        const size_t at = ((size_t)b * a.T + t0) * a.H + h;
-        if (!STATES_ONLY) stage<DK>(sQ, q + at * DK, (size_t)a.H * DK, c, tid);
-        stage<DK>(sK, k + at * DK, (size_t)a.H * DK, c, tid);
-        stage<DV>(sV, v + at * DV, (size_t)a.H * DV, c, tid);
+        int t0, c;
+        tokens_of(it, t0, c);
+        if (it > n0) {
+            __syncthreads();                    // the chunk before is consumed
+            load(it);
+        }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
 
         if (!STATES_ONLY) {
-            // ---- P_ij = f_intra lambda^|i-j| (q_i . k_j) on the causal side; rows ty + 16 a, columns tx + 16 b
-            float s[4][4] = {};
+            // ---- P_ij = f_intra lambda^(i-j) (q_i . k_j), j <= i; columns 32 wc + cx + 8 b.  Tiles
+            // that no pair j <= i falls into are left out, here and in P V.
+            if (2 * wc <= wr) {
+                float s[4][4] = {};
 #pragma unroll 4
-            for (int d = 0; d < DK; d += 4) {
-                float4 x[4], y[4];
+                for (int d = 0; d < DK; d += 4) {
+                    float4 x[4], y[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = la_load4(sQ + (ty + 16 * i) * PK + d);
+                    for (int i = 0; i < 4; ++i) x[i] = la_load4(sQ + (row0 + 4 * i) * PK + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = la_load4(sK + (tx + 16 * j) * PK + d);
+                    for (int j = 0; j < 4; ++j) y[j] = la_load4(sK + (32 * wc + cx + 8 * j) * PK + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = row0 + 4 * i, m = 32 * wc + cx + 8 * j;
+                        sP[r * PP + m] = r >= m ? s[i][j] * (sW[max(r - m, 0)] * ps.f_intra) : 0.f;
+                    }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = ty + 16 * i, m = tx + 16 * j, ahead = rev ? m - r : r - m;
-                    sP[r * PP + m] = ahead >= 0 ? s[i][j] * (sW[max(ahead, 0)] * ps.f_intra) : 0.f;
-                }
             __syncthreads();
-            // ---- out rows ty + 16 a, columns 4 tx + 64 b: P V + lambda^(.) Q S
+            // ---- out: P V + lambda^(.) Q S
             float4 o[4][CV], x[4][CV];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int m = 0; m < CV; ++m) o[i][m] = x[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-            for (int j = 0; j < kC; j += 4) {
+            for (int j = 0; j < 16 * wr + 16; j += 4) {
                 float4 p[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = la_load4(sP + (ty + 16 * i) * PP + j);
+                for (int i = 0; i < 4; ++i) p[i] = la_load4(sP + (row0 + 4 * i) * PP + j);
 #pragma unroll
                 for (int m = 0; m < CV; ++m)
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
-                        const float4 y = la_load4(sV + (j + jj) * PV + 4 * tx + 64 * m);
+                        const float4 y = la_load4(sV + (j + jj) * PV + col4 + 64 * m);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             fma4(o[i][m], jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w, y);
@@ -205,12 +238,12 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
             for (int d = 0; d < DK; d += 4) {
                 float4 p[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = la_load4(sQ + (ty + 16 * i) * PK + d);
+                for (int i = 0; i < 4; ++i) p[i] = la_load4(sQ + (row0 + 4 * i) * PK + d);
 #pragma unroll
                 for (int m = 0; m < CV; ++m)
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
-                        const float4 y = la_load4(sS + (d + jj) * PV + 4 * tx + 64 * m);
+                        const float4 y = la_load4(sS + (d + jj) * PV + col4 + 64 * m);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             fma4(x[i][m], jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w, y);
@@ -219,10 +252,10 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
             InT *out = static_cast<InT *>(ps.out);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = ty + 16 * i;
+                const int r = row0 + 4 * i;
                 if (r >= c) continue;
-                const float f = ps.f_inter * sW[rev ? c - 1 - r : r + 1];
-                const size_t g = (((size_t)b * a.T + t0 + r) * a.H + h) * DV + 4 * tx;
+                const float f = ps.f_inter * sW[rev ? r : r + 1];
+                const size_t g = token_at(t0, c, r) * DV + col4;
 #pragma unroll
                 for (int m = 0; m < CV; ++m) {
                     fma4(o[i][m], f, x[i][m]);
@@ -232,9 +265,14 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
             __syncthreads();                    // every reader of the state and of k is done
         }
         // ---- k_j <- f_write lambda^(.) k_j, then S <- lambda^c S + K'^T V
-        for (int e = tid; e < kC * DK; e += kThreads) {
-            const int t = e / DK;
-            if (t < c) sK[t * PK + e % DK] *= ps.f_write * sW[rev ? t + 1 : c - 1 - t];
+#pragma unroll
+        for (int e = 0; e < kC * DK / 4 / kThreads; ++e) {
+            const int id = e * kThreads + tid, t = id / (DK / 4);
+            float *p = sK + t * PK + 4 * (id % (DK / 4));
+            const float w = ps.f_write * sW[max(rev ? c - t : c - 1 - t, 0)];
+            float4 x = la_load4(p);
+            x.x *= w; x.y *= w; x.z *= w; x.w *= w;
+            la_store4(p, x);
         }
         __syncthreads();
         float4 u[RK][CV];
@@ -242,15 +280,16 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
         for (int r = 0; r < RK; ++r)
 #pragma unroll
             for (int m = 0; m < CV; ++m) u[r][m] = make_float4(0.f, 0.f, 0.f, 0.f);
-        // rows 4 ty + 64 r4 + {0..3}: RK = 4 or 8 rows in RK / 4 groups
-#pragma unroll 2
+        // rows 4 (4 wr + ry) + 64 g + {0..3}: RK = 4 or 8 rows in RK / 4 groups
+        const int srow = 16 * wr + 4 * ry;
+#pragma unroll (RK * CV > 8 ? 2 : 8)
         for (int j = 0; j < kC; ++j) {
             float4 y[CV];
 #pragma unroll
-            for (int m = 0; m < CV; ++m) y[m] = la_load4(sV + j * PV + 4 * tx + 64 * m);
+            for (int m = 0; m < CV; ++m) y[m] = la_load4(sV + j * PV + col4 + 64 * m);
 #pragma unroll
             for (int g = 0; g < RK / 4; ++g) {
-                const float4 x = la_load4(sK + j * PK + 4 * ty + 64 * g);
+                const float4 x = la_load4(sK + j * PK + srow + 64 * g);
 #pragma unroll
                 for (int m = 0; m < CV; ++m) {
                     fma4(u[4 * g][m], x.x, y[m]);
@@ -265,7 +304,7 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
         for (int r = 0; r < RK; ++r)
 #pragma unroll
             for (int m = 0; m < CV; ++m) {
-                float *p = sS + (4 * ty + 64 * (r / 4) + r % 4) * PV + 4 * tx + 64 * m;
+                float *p = sS + (srow + 64 * (r / 4) + r % 4) * PV + col4 + 64 * m;
                 const float4 s = la_load4(p);
                 fma4(u[r][m], lo, s);
                 fma4(u[r][m], hi, s);
