@@ -1,14 +1,16 @@
-// Linear attention with one decay per head on CUDA cores, fp32 arithmetic throughout
-// (the mathematics is in kda_la.cuh).
+// Linear attention with one decay per head on warp matrix instructions: fp32 for all head
+// dimensions, bf16 where one is 64 (the mathematics is in kda_la.cuh).
 //
 // One CTA walks the chunks of 64 tokens of one (pass, b, h, segment) with the state
-// resident in shared memory.  A chunk is four small products of register tiles:
-// 64 x 64 scores (4 x 4 a thread), the outputs P V + Q S (4 rows x DV/16 columns a
-// thread) and the state K'^T V (DK/16 x DV/16 a thread), operands read as 16-byte
-// vectors of padded rows.  A chunk's 8 dk dv + .. multiply-adds are what bounds it (4.3 us a
-// chunk of 64-channel heads at the SM's full rate), so the tile loads of a chunk are all under
-// way together and two CTAs share an SM where they fit.  Powers of lambda are computed in 64
-// bits once per CTA, so their rounding does not grow along the sequence.
+// resident in shared memory as fp32.  A chunk is four products of 64-wide tiles, Q K^T, P V,
+// Q S and K'^T V; of each tile a warp has 16 rows and 32 columns.  Operands are fp32 in shared
+// memory and go in as two tf32 parts, so the sums keep fp32's accuracy.  Multiply-adds on CUDA
+// cores with 4 x 4 register tiles were bound by shared memory, 3 wavefronts to 4 x 32
+// multiply-adds of a 16-byte read (B4 T2048 H32 d128 fp32 695 us, B8 T2048 H32 d64 bf16 468):
+// here they are 528 and 271, the tensor pipe is half busy and the waits are its own and the
+// barriers'.  A chunk's loads are all under way together, ahead of the state's update, and
+// two CTAs share an SM where they fit.  Powers of lambda are computed in 64 bits once per CTA,
+// so their rounding does not grow along the sequence.
 #include "kda_la.cuh"
 
 namespace kda {
@@ -19,7 +21,7 @@ constexpr int kThreads = 256;
 
 template <int DK, int DV>
 struct LaSmem {
-    static constexpr int PK = DK + 4, PV = DV + 4, PP = kC + 4;   // row pitches: 16-byte aligned, 4 banks apart
+    static constexpr int PK = DK + 8, PV = DV + 4, PP = kC + 8;   // row pitches; see mma_split
     static constexpr int off_q = 0;
     static constexpr int off_k = off_q + kC * PK;
     static constexpr int off_v = off_k + kC * PK;
@@ -35,27 +37,84 @@ __device__ __forceinline__ void fma4(float4 &acc, float a, float4 b)
 {
     acc.x += a * b.x; acc.y += a * b.y; acc.z += a * b.z; acc.w += a * b.w;
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b, float acc)
+
+// ---- products on warp matrix instructions (m16n8k8, tf32 operands, fp32 accumulators).  An fp32
+// operand goes in as two tf32 parts of 11 bits: hi is the nearest, lo the rest with its last bits
+// cut off, 2^-22 of x at most and of either sign.  Of the four products of parts lo lo is left
+// out, 2^-22 of a term.  A NaN stays one: where the sum that rounds hi runs over, lo is the NaN.
+// (Rounding lo as well, by conversion instructions, left the same errors: 23.7 us for 22.8 at
+// B2 T1023 H8 d64.)  What is bf16 is its own hi.
+//
+// Lane (g, t) = (lane / 4, lane % 4) holds rows g, g + 8 of A, column g of B, and of both the
+// depths 2 t, 2 t + 1 of a step's 8 (the order of the depths is free as long as A and B agree).
+// Operands that lie [row][depth] are read as pairs: pitches of 8 banks a row spread them over all
+// banks.  [depth][column] ones are read as words from rows 2 t and 2 t + 1: there it is 4 banks.
+struct Parts { uint32_t hi, lo; };
+template <bool EXACT> __device__ __forceinline__ Parts parts_of(float x)
 {
-    acc += a.x * b.x; acc += a.y * b.y; acc += a.z * b.z; acc += a.w * b.w;
-    return acc;
+    if (EXACT) return {__float_as_uint(x), 0u};
+    const uint32_t hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+    return {hi, __float_as_uint(x - __uint_as_float(hi)) & 0xffffe000u};
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// c[n] += A B_n over 8 depths.  The matrix instruction cuts what it adds to its accumulator off
+// instead of rounding it, so each step's sum starts from zero, with the small products, and is
+// added to c by an fp32 addition: one accumulator over all depths left 1.7e-6 of an output's
+// norm where this leaves 1.8e-7, for 3 to 9 % of the time.  COARSE: one accumulator (an output
+// that is rounded to bf16).  x0, x1: A's rows g and g + 8 at the lane's two depths; y[n]: B_n's
+// column at them.
+template <bool A_EXACT, bool B_EXACT, bool COARSE, int N>
+__device__ __forceinline__ void mma_split(float (*c)[4], float2 x0, float2 x1, const float2 (&y)[N])
+{
+    const Parts p[4] = {parts_of<A_EXACT>(x0.x), parts_of<A_EXACT>(x1.x), parts_of<A_EXACT>(x0.y), parts_of<A_EXACT>(x1.y)};
+    const uint32_t hi[4] = {p[0].hi, p[1].hi, p[2].hi, p[3].hi}, lo[4] = {p[0].lo, p[1].lo, p[2].lo, p[3].lo};
+    Parts q[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n) { q[n][0] = parts_of<B_EXACT>(y[n].x); q[n][1] = parts_of<B_EXACT>(y[n].y); }
+    float fresh[N][4] = {};
+    float (*sum)[4] = COARSE ? c : fresh;
+    if (!B_EXACT)
+#pragma unroll
+        for (int n = 0; n < N; ++n) mma_tf32(sum[n], hi, q[n][0].lo, q[n][1].lo);
+    if (!A_EXACT)
+#pragma unroll
+        for (int n = 0; n < N; ++n) mma_tf32(sum[n], lo, q[n][0].hi, q[n][1].hi);
+#pragma unroll
+    for (int n = 0; n < N; ++n) mma_tf32(sum[n], hi, q[n][0].hi, q[n][1].hi);
+    if (!COARSE)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[n][i] += fresh[n][i];
+}
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+template <typename T> __device__ __forceinline__ void store_pair(T *p, float x, float y);
+template <> __device__ __forceinline__ void store_pair<float>(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+template <> __device__ __forceinline__ void store_pair<__nv_bfloat16>(__nv_bfloat16 *p, float x, float y)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
 }
 
 // A chunk's rows of D channels to shared memory as fp32, in the order of the walk: row t is
 // token t (forward) or c - 1 - t (reversed), rows from c on are zeros.  `src` is row 0's, `step`
 // leads to the next.  The loads are all issued before the first is needed.
-template <int D>
+template <int D, int PITCH>
 __device__ __forceinline__ void stage(float *dst, const float *src, ptrdiff_t step, int c, int tid)
 {
 #pragma unroll
     for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
         const int id = e * kThreads + tid, t = id / (D / 4), x = 4 * (id % (D / 4));
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + t * (D + 4) + x);
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + t * PITCH + x);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                      :: "r"(to), "l"(src + (t < c ? t * step + x : 0)), "r"(t < c ? 16 : 0) : "memory");
     }
 }
-template <int D>
+template <int D, int PITCH>
 __device__ __forceinline__ void stage(float *dst, const __nv_bfloat16 *src, ptrdiff_t step, int c, int tid)
 {
     float4 v[kC * D / 4 / kThreads];
@@ -67,31 +126,30 @@ __device__ __forceinline__ void stage(float *dst, const __nv_bfloat16 *src, ptrd
 #pragma unroll
     for (int e = 0; e < kC * D / 4 / kThreads; ++e) {
         const int id = e * kThreads + tid;
-        la_store4(dst + (id / (D / 4)) * (D + 4) + 4 * (id % (D / 4)), v[e]);
+        la_store4(dst + (id / (D / 4)) * PITCH + 4 * (id % (D / 4)), v[e]);
     }
 }
 
 // CTAs of an SM: two where the shared memory of both fits
-template <int DK, int DV> constexpr int simt_resident() { return LaSmem<DK, DV>::bytes <= 112 * 1024 ? 2 : 1; }
+template <int DK, int DV> constexpr int mma_resident() { return LaSmem<DK, DV>::bytes <= 112 * 1024 ? 2 : 1; }
 
 template <int DK, int DV, typename InT, bool STATES_ONLY>
-__global__ void __launch_bounds__(kThreads, simt_resident<DK, DV>())
-la_simt_kernel(const __grid_constant__ LaArgs a)
+__global__ void __launch_bounds__(kThreads, mma_resident<DK, DV>())
+la_mma_kernel(const __grid_constant__ LaArgs a)
 {
     using L = LaSmem<DK, DV>;
     constexpr int PK = L::PK, PV = L::PV, PP = L::PP;
-    constexpr int RK = DK / 16, CV = DV / 64;   // state rows, float4 column groups per thread
+    constexpr bool EX = sizeof(InT) == 2;       // q, k, v are exact in one part
+    constexpr int GK = DK / 64, CV = DV / 64;   // groups of 64 state rows and of 64 columns
     extern __shared__ __align__(16) float sm[];
     float *sQ = sm + L::off_q, *sK = sm + L::off_k, *sV = sm + L::off_v, *sP = sm + L::off_p, *sS = sm + L::off_s;
     float *sW = sm + L::off_w;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // A product's 64 x 64 tile: warp w has rows 16 wr .. and columns 32 wc .., a lane 4 rows and 4
-    // columns of them, so that a warp's 16-byte reads of an operand are 64 or 128 bytes of different
-    // banks.  Warps w and w + 4 share a scheduler: together they have as many causal pairs as any two.
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wr = warp < 4 ? warp : 7 - warp, wc = warp >> 2, ry = lane >> 3, cx = lane & 7;
-    const int row0 = 16 * wr + ry, col4 = 32 * wc + 4 * cx;     // rows row0 + 4 i; channels col4 + 64 m ..
+    // Of a product's 64 x 64 tile warp w has rows 16 wr .. and columns 32 wc ..  Warps w and w + 4
+    // share a scheduler: together they have as many causal pairs as any two.
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t2 = 2 * (lane & 3);
+    const int wr = warp < 4 ? warp : 7 - warp, wc = warp >> 2, row = 16 * wr + g, col = 32 * wc;
     const int nwork = STATES_ONLY ? a.nseg - 1 : a.nseg;
     const int seg = blockIdx.x % nwork;
     const int bh = (blockIdx.x / nwork) % (a.B * a.H);
@@ -122,9 +180,9 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
         tokens_of(it, t0, c);
         const size_t at = token_at(t0, c, 0);
         const ptrdiff_t step = rev ? -(ptrdiff_t)a.H : (ptrdiff_t)a.H;
-        if (!STATES_ONLY) stage<DK>(sQ, q + at * DK, step * DK, c, tid);
-        stage<DK>(sK, k + at * DK, step * DK, c, tid);
-        stage<DV>(sV, v + at * DV, step * DV, c, tid);
+        if (!STATES_ONLY) stage<DK, PK>(sQ, q + at * DK, step * DK, c, tid);
+        stage<DK, PK>(sK, k + at * DK, step * DK, c, tid);
+        stage<DV, PV>(sV, v + at * DV, step * DV, c, tid);
     };
     load(n0);                               // under way while the entering state is made
     // ---- entering state.  One segment, and segment 0 of the walk without outputs: the initial
@@ -149,12 +207,12 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
                 s[i] = seg == 0 ? la_load4(slots + (size_t)(a.nseg - 1) * DK * DV + e0 + 4 * i * kThreads)
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int g = 0; g < seg; ++g)
+            for (int x = 0; x < seg; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float4 u = la_load4(slots + (size_t)g * DK * DV + e0 + 4 * i * kThreads);
-                    fma4(s[i], weight[2 * g + 1], u);
-                    fma4(s[i], weight[2 * g], u);
+                    const float4 u = la_load4(slots + (size_t)x * DK * DV + e0 + 4 * i * kThreads);
+                    fma4(s[i], weight[2 * x + 1], u);
+                    fma4(s[i], weight[2 * x], u);
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -180,136 +238,108 @@ la_simt_kernel(const __grid_constant__ LaArgs a)
     for (int it = n0; it < n1; ++it) {
         int t0, c;
         tokens_of(it, t0, c);
-        if (it > n0) {
-            __syncthreads();                    // the chunk before is consumed
-            load(it);
-        }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncthreads();
+        __syncthreads();                        // the chunk's rows and the state are there
 
         if (!STATES_ONLY) {
-            // ---- P_ij = f_intra lambda^(i-j) (q_i . k_j), j <= i; columns 32 wc + cx + 8 b.  Tiles
-            // that no pair j <= i falls into are left out, here and in P V.
+            // ---- P_ij = f_intra lambda^(i-j) (q_i . k_j), j <= i.  Tiles that no pair j <= i falls
+            // into are left out, here and in P V.
             if (2 * wc <= wr) {
                 float s[4][4] = {};
-#pragma unroll 4
-                for (int d = 0; d < DK; d += 4) {
-                    float4 x[4], y[4];
+#pragma unroll 2
+                for (int d = t2; d < DK; d += 8) {
+                    float2 y[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = la_load4(sQ + (row0 + 4 * i) * PK + d);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = la_load4(sK + (32 * wc + cx + 8 * j) * PK + d);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[i][j] = dot4(x[i], y[j], s[i][j]);
+                    for (int n = 0; n < 4; ++n) y[n] = load2(sK + (col + 8 * n + g) * PK + d);
+                    mma_split<EX, EX, EX>(s, load2(sQ + row * PK + d), load2(sQ + (row + 8) * PK + d), y);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = row0 + 4 * i, m = 32 * wc + cx + 8 * j;
-                        sP[r * PP + m] = r >= m ? s[i][j] * (sW[max(r - m, 0)] * ps.f_intra) : 0.f;
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = row + 8 * i, m = col + 8 * n + t2, apart = r - m;
+                        *reinterpret_cast<float2 *>(sP + r * PP + m) =
+                            make_float2(apart >= 0 ? s[n][2 * i] * (sW[max(apart, 0)] * ps.f_intra) : 0.f,
+                                        apart >= 1 ? s[n][2 * i + 1] * (sW[max(apart - 1, 0)] * ps.f_intra) : 0.f);
                     }
             }
             __syncthreads();
-            // ---- out: P V + lambda^(.) Q S
-            float4 o[4][CV], x[4][CV];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int m = 0; m < CV; ++m) o[i][m] = x[i][m] = make_float4(0.f, 0.f, 0.f, 0.f);
+            // ---- out: P V + (f_inter lambda^(.) Q) S
+            float o[4 * CV][4] = {};
 #pragma unroll 2
-            for (int j = 0; j < 16 * wr + 16; j += 4) {
-                float4 p[4];
+            for (int j = t2; j < 16 * wr + 16; j += 8) {
+                const float2 x0 = load2(sP + row * PP + j), x1 = load2(sP + (row + 8) * PP + j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = la_load4(sP + (row0 + 4 * i) * PP + j);
+                for (int m = 0; m < CV; ++m) {
+                    float2 y[4];
 #pragma unroll
-                for (int m = 0; m < CV; ++m)
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj) {
-                        const float4 y = la_load4(sV + (j + jj) * PV + col4 + 64 * m);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            fma4(o[i][m], jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w, y);
+                    for (int n = 0; n < 4; ++n) {
+                        const float *p = sV + j * PV + col + 64 * m + 8 * n + g;
+                        y[n] = make_float2(p[0], p[PV]);
                     }
+                    mma_split<false, EX, EX>(o + 4 * m, x0, x1, y);
+                }
             }
-#pragma unroll 2
-            for (int d = 0; d < DK; d += 4) {
-                float4 p[4];
+            const float f0 = ps.f_inter * sW[rev ? row : row + 1], f1 = ps.f_inter * sW[rev ? row + 8 : row + 9];
+#pragma unroll (CV > 1 ? 1 : 2)
+            for (int d = t2; d < DK; d += 8) {
+                float2 x0 = load2(sQ + row * PK + d), x1 = load2(sQ + (row + 8) * PK + d);
+                x0.x *= f0; x0.y *= f0; x1.x *= f1; x1.y *= f1;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[i] = la_load4(sQ + (row0 + 4 * i) * PK + d);
+                for (int m = 0; m < CV; ++m) {
+                    float2 y[4];
 #pragma unroll
-                for (int m = 0; m < CV; ++m)
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj) {
-                        const float4 y = la_load4(sS + (d + jj) * PV + col4 + 64 * m);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            fma4(x[i][m], jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w, y);
+                    for (int n = 0; n < 4; ++n) {
+                        const float *p = sS + d * PV + col + 64 * m + 8 * n + g;
+                        y[n] = make_float2(p[0], p[PV]);
                     }
+                    mma_split<false, false, EX>(o + 4 * m, x0, x1, y);
+                }
             }
             InT *out = static_cast<InT *>(ps.out);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = row0 + 4 * i;
-                if (r >= c) continue;
-                const float f = ps.f_inter * sW[rev ? r : r + 1];
-                const size_t g = token_at(t0, c, r) * DV + col4;
+            for (int i = 0; i < 2; ++i)
+                if (row + 8 * i < c) {
+                    InT *p = out + token_at(t0, c, row + 8 * i) * DV + col + t2;
 #pragma unroll
-                for (int m = 0; m < CV; ++m) {
-                    fma4(o[i][m], f, x[i][m]);
-                    la_store4(out + g + 64 * m, o[i][m]);
+                    for (int n = 0; n < 4 * CV; ++n) store_pair(p + 64 * (n / 4) + 8 * (n % 4), o[n][2 * i], o[n][2 * i + 1]);
                 }
+        }
+        // ---- U = K'^T V with k'_j = f_write lambda^(.) k_j
+        float u[GK * CV * 4][4] = {};
+        const int fade = rev ? c : c - 1;
+#pragma unroll 2
+        for (int j = t2; j < kC; j += 8) {
+            const float w0 = ps.f_write * sW[max(fade - j, 0)], w1 = ps.f_write * sW[max(fade - j - 1, 0)];
+            float2 y[4 * CV];
+#pragma unroll
+            for (int n = 0; n < 4 * CV; ++n) {
+                const float *p = sV + j * PV + col + 64 * (n / 4) + 8 * (n % 4) + g;
+                y[n] = make_float2(p[0], p[PV]);
             }
-            __syncthreads();                    // every reader of the state and of k is done
-        }
-        // ---- k_j <- f_write lambda^(.) k_j, then S <- lambda^c S + K'^T V
 #pragma unroll
-        for (int e = 0; e < kC * DK / 4 / kThreads; ++e) {
-            const int id = e * kThreads + tid, t = id / (DK / 4);
-            float *p = sK + t * PK + 4 * (id % (DK / 4));
-            const float w = ps.f_write * sW[max(rev ? c - t : c - 1 - t, 0)];
-            float4 x = la_load4(p);
-            x.x *= w; x.y *= w; x.z *= w; x.w *= w;
-            la_store4(p, x);
-        }
-        __syncthreads();
-        float4 u[RK][CV];
-#pragma unroll
-        for (int r = 0; r < RK; ++r)
-#pragma unroll
-            for (int m = 0; m < CV; ++m) u[r][m] = make_float4(0.f, 0.f, 0.f, 0.f);
-        // rows 4 (4 wr + ry) + 64 g + {0..3}: RK = 4 or 8 rows in RK / 4 groups
-        const int srow = 16 * wr + 4 * ry;
-#pragma unroll (RK * CV > 8 ? 2 : 8)
-        for (int j = 0; j < kC; ++j) {
-            float4 y[CV];
-#pragma unroll
-            for (int m = 0; m < CV; ++m) y[m] = la_load4(sV + j * PV + col4 + 64 * m);
-#pragma unroll
-            for (int g = 0; g < RK / 4; ++g) {
-                const float4 x = la_load4(sK + j * PK + srow + 64 * g);
-#pragma unroll
-                for (int m = 0; m < CV; ++m) {
-                    fma4(u[4 * g][m], x.x, y[m]);
-                    fma4(u[4 * g + 1][m], x.y, y[m]);
-                    fma4(u[4 * g + 2][m], x.z, y[m]);
-                    fma4(u[4 * g + 3][m], x.w, y[m]);
-                }
+            for (int k = 0; k < GK; ++k) {
+                const float *p = sK + j * PK + row + 64 * k;
+                mma_split<false, EX, false>(u + 4 * CV * k, make_float2(w0 * p[0], w1 * p[PK]), make_float2(w0 * p[8], w1 * p[PK + 8]), y);
             }
         }
+        __syncthreads();                        // every reader of the rows and of the state is done
+        if (it + 1 < n1) load(it + 1);
+        // ---- S <- lambda^c S + U
         const float hi = sm[L::off_l + (c == kC ? 0 : 2)], lo = sm[L::off_l + (c == kC ? 1 : 3)];
 #pragma unroll
-        for (int r = 0; r < RK; ++r)
+        for (int k = 0; k < GK; ++k)
 #pragma unroll
-            for (int m = 0; m < CV; ++m) {
-                float *p = sS + (srow + 64 * (r / 4) + r % 4) * PV + col4 + 64 * m;
-                const float4 s = la_load4(p);
-                fma4(u[r][m], lo, s);
-                fma4(u[r][m], hi, s);
-                la_store4(p, u[r][m]);
-            }
+            for (int n = 0; n < 4 * CV; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float2 *p = reinterpret_cast<float2 *>(sS + (row + 8 * i + 64 * k) * PV + col + 64 * (n / 4) + 8 * (n % 4) + t2);
+                    float2 x = make_float2(u[4 * CV * k + n][2 * i], u[4 * CV * k + n][2 * i + 1]);
+                    const float2 s = *p;
+                    x.x += lo * s.x; x.y += lo * s.y;
+                    x.x += hi * s.x; x.y += hi * s.y;
+                    *p = x;
+                }
     }
     __syncthreads();
     // ---- leaving state
@@ -343,7 +373,7 @@ cudaError_t launch_behind(Kernel kernel, size_t grid, size_t smem, const LaArgs 
 template <int DK, int DV, typename InT, bool STATES_ONLY>
 cudaError_t launch_typed(const LaArgs &a, cudaStream_t stream)
 {
-    auto kernel = la_simt_kernel<DK, DV, InT, STATES_ONLY>;
+    auto kernel = la_mma_kernel<DK, DV, InT, STATES_ONLY>;
     constexpr size_t bytes = LaSmem<DK, DV>::bytes;
     static OncePerDevice once;
     cudaError_t e = set_shared_memory(kernel, (int)bytes, once);
@@ -363,9 +393,9 @@ cudaError_t launch_dims(const LaArgs &a, cudaStream_t stream)
     return cudaErrorInvalidValue;
 }
 
-// fp32 arithmetic on CUDA cores.  states_only: each segment's own contribution to the state
+// states_only: each segment's own contribution to the state
 // (all but the last's) goes to its slot of a.ws, [npass][B * H][nseg][dk][dv] fp32, no outputs.
-cudaError_t launch_la_simt(const LaArgs &a, bool states_only, cudaStream_t stream)
+cudaError_t launch_la_mma(const LaArgs &a, bool states_only, cudaStream_t stream)
 {
     if (a.dtype == KDA_BF16)
         return states_only ? launch_dims<__nv_bfloat16, true>(a, stream) : launch_dims<__nv_bfloat16, false>(a, stream);
@@ -384,8 +414,8 @@ void la_choose_segments(LaArgs &a)
     constexpr int kMaxSegments = 32;        // a warp's lanes look at them
     const bool tc = la_tc_supported(a.dk, a.dv, a.dtype);
     const int C = tc ? 128 : kC;
-    const int places = 148 * (!tc && a.dk == 64 && a.dv == 64 ? simt_resident<64, 64>() : 1);
-    const double state_cost = tc ? 0.6 : 0.5, join_cost = tc ? 3.0 : 1.0, per_segment = tc ? 0.5 : 0.05;
+    const int places = 148 * (!tc && a.dk == 64 && a.dv == 64 ? mma_resident<64, 64>() : 1);
+        const double state_cost = tc ? 0.6 : 0.5, join_cost = tc ? 3.0 : 1.0, per_segment = tc ? 0.5 : 0.05;
     const int chunks = (a.T + C - 1) / C;
     const long long heads = (long long)a.npass * a.B * a.H;
     a.nseg = 1;
@@ -409,15 +439,15 @@ size_t la_workspace_bytes(const LaArgs &a)
     return a.nseg > 1 ? sizeof(float) * (size_t)a.npass * a.B * a.H * a.nseg * a.dk * a.dv : 0;
 }
 
-// CUDA cores with nseg > 1: every segment's own contribution, then the outputs.
+// Warp matrix instructions with nseg > 1: every segment's own contribution, then the outputs.
 cudaError_t launch_la(const LaArgs &a, cudaStream_t stream)
 {
     if (la_tc_supported(a.dk, a.dv, a.dtype)) return launch_la_tc(a, stream);
     if (a.nseg > 1) {
-        const cudaError_t e = launch_la_simt(a, true, stream);
+        const cudaError_t e = launch_la_mma(a, true, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_la_simt(a, false, stream);
+    return launch_la_mma(a, false, stream);
 }
 
 }  // namespace kda

@@ -493,7 +493,7 @@ size_t kda_backward_workspace_bytes(int B, int T, int H, int dk, int dv);
  * reach the outputs of earlier tokens of its chunk (128 tokens).
  *
  * Supported: dk, dv in {64, 128}, both dtypes; bf16 with dk = dv = 128 runs on the
- * tensor cores, anything else in fp32 on CUDA cores.  B, H >= 1, T >= 0; T = 0 writes no
+ * tensor cores, anything else with fp32 operands in two parts each.  B, H >= 1, T >= 0; T = 0 writes no
  * output and sets final_state to initial_state (or zeros).  A workspace that is missing
  * or too small: KDA_ERR_INVALID_ARG; misaligned: KDA_ERR_MISALIGNED.  Asynchronous on
  * `stream`; deterministic; may be captured into a graph.

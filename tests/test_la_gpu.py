@@ -221,6 +221,21 @@ def test_a_sequence_padded_with_zeros(dtype, length):
     assert float((at_end - padded[:1]).norm()) <= 2e-5 * float(at_end.norm())
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("f32", 128), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("bits", ["nan", "all ones", "inf"])
+def test_what_is_not_finite_is_not_lost(dtype, d, bits):
+    for n, after in (("q", False), ("k", True), ("v", True)):
+        x = _inputs(1, 300, 1, d, d, dtype, 23, decay=-0.01)
+        if bits == "all ones":
+            x[n].view(torch.int32 if dtype == "f32" else torch.int16)[0, 200, 0, 5] = 0x7fffffff if dtype == "f32" else 0x7fff
+        else:
+            x[n][0, 200, 0, 5] = float(bits)
+        out, last = _forward(x)
+        lost = torch.isfinite(out[0, :, 0]).all(-1)
+        assert not lost[200] and not (after and lost[200:].any())
+        assert torch.isfinite(last).all() == (not after) and bool(lost[:128].all())
+
+
 def test_no_tokens():
     x = _inputs(2, 0, 3, 128, 128, "bf16", 12)
     out, last = _forward(x)
