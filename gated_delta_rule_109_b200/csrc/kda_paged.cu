@@ -358,7 +358,7 @@ struct SimtState {
 
 template <int D, typename InT, int HG, int HW>
 __global__ void __launch_bounds__(kThreads)
-paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
+paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page, const bool whole_rows)
 {
     using L = PagedSmem<D, InT, HG>;
     constexpr int CPR = D * (int)sizeof(InT) / 16;      // 16-byte pieces of a row
@@ -376,14 +376,35 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page)
 
     const int group = a.H / a.Hkv, blocks = (group + HG - 1) / HG;
     const unsigned long long per = (unsigned long long)(a.Hkv / HW) * blocks;
-    const RowAt at = find_row<HW>(a, per, blockIdx.x, gridDim.x, -1);
-    const unsigned long long owners = owners_of(at.total, gridDim.x);
-    if (blockIdx.x >= owners) return;
-    unsigned long long u = (unsigned long long)blockIdx.x * at.total / owners;
-    const unsigned long long u1 = ((unsigned long long)blockIdx.x + 1) * at.total / owners;
-
-    int b = at.b, part = 0, n = at.keys, tiles = tiles_of<HW>(n);
-    unsigned long long row_first = at.first;
+    // this CTA's units [u, u1), the first of them in row b, whose own begin at row_first
+    unsigned long long u, u1, row_first;
+    int b, n, part = 0, tiles;
+    if (whole_rows) {
+        const unsigned int hb = blockIdx.x % (unsigned int)per;
+        b = blockIdx.x / (unsigned int)per;
+        n = row_keys(a, b);
+        tiles = tiles_of<HW>(n);
+        row_first = 0;
+        u = (unsigned long long)hb * tiles;
+        u1 = u + tiles;
+        if (n == 0) {                                   // no keys: zeros
+            const int blk0 = (int)(hb % blocks) * HG, nh = min(HG, group - blk0);
+            for (int e = tid; e < HW * nh * D; e += kThreads) {
+                const size_t head = (size_t)b * a.H + (hb / blocks * HW + e / (nh * D)) * group + blk0 + e / D % nh;
+                static_cast<InT *>(a.out)[head * D + e % D] = la_round<InT>(0.f);
+            }
+        }
+    } else {
+        const RowAt at = find_row<HW>(a, per, blockIdx.x, gridDim.x, -1);
+        const unsigned long long owners = owners_of(at.total, gridDim.x);
+        if (blockIdx.x >= owners) return;
+        u = (unsigned long long)blockIdx.x * at.total / owners;
+        u1 = ((unsigned long long)blockIdx.x + 1) * at.total / owners;
+        b = at.b;
+        n = at.keys;
+        tiles = tiles_of<HW>(n);
+        row_first = at.first;
+    }
     while (u < u1) {
         while (u >= row_first + per * tiles) {          // next row that has units
             row_first += per * tiles;
@@ -621,6 +642,24 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
 template <int D, typename InT, int HG>
 constexpr int resident() { return 226 * 1024 / (PagedSmem<D, InT, HG>::total + 1024); }
 
+// Whether each CTA takes one row whole (for its heads): nothing is left to join then, and no CTA
+// empties its pipeline at a row's end to fill it again.  It pays for many rows and for short ones;
+// for few long ones the CTAs share the keys.  What the host knows are the table's bounds: with
+// `most` units to a row the first form takes about 6 us and a unit's time for every unit of every
+// wave of CTAs, the second 12 us, its share of the units, and 14 us for every row that begins in
+// a CTA's share.  In a graph, us, shared / whole (32 / 8 heads of 128 bf16, rows up to L keys, drawn):
+// 64 rows, L 250 32 / 15, L 1000 53 / 37; 128 rows, L 450 64 / 33, L 5000 259 / 270;
+// 16 rows, L 450 19 / 17, L 2500 27 / 59; one row, L 500 11.5 / 16.2.
+template <int D, typename InT, int HG, int HW>
+bool takes_whole_rows(const PagedArgs &a)
+{
+    constexpr int R = resident<D, InT, HG>();
+    constexpr double unit = R == 1 ? 1.6 : R == 2 ? 0.62 : 0.42;       // us, with R CTAs on an SM
+    const double stretches = (double)a.B * (a.Hkv / HW) * ((a.H / a.Hkv + HG - 1) / HG), share = stretches / (kSms * R);
+    const double most = ceil((double)a.max_pages * a.page_size / unit_keys<HW>());
+    return 6 + unit * most * ceil(share) <= 12 + (unit * most + 14) * share;
+}
+
 // Query heads that share one reading of the cache.  bf16: 8 columns of a product, or two
 // times 8 for larger groups (a third would no longer fit the registers); fp32: as many as the
 // group has, up to 8.
@@ -645,7 +684,9 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
     cudaError_t e = set_shared_memory(kernel, L::total, once);
     if (e != cudaSuccess) return e;
     static_assert(resident<D, InT, HG>() <= kMaxResident, "the workspace holds two stretches per CTA");
-    const unsigned int grid = kSms * resident<D, InT, HG>();
+    unsigned int grid = kSms * resident<D, InT, HG>();
+    const bool whole_rows = takes_whole_rows<D, InT, HG, HW>(a);
+    if (whole_rows) grid = (unsigned int)((size_t)a.B * (a.Hkv / HW) * ((a.H / a.Hkv + HG - 1) / HG));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -656,8 +697,9 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, divider((unsigned int)a.page_size))) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, kernel, a, divider((unsigned int)a.page_size), whole_rows)) != cudaSuccess) return e;
     note_launch();
+    if (whole_rows) return cudaGetLastError();
     cfg.gridDim = dim3((unsigned)((size_t)a.B * a.H));
     cfg.dynamicSmemBytes = 0;
     if ((e = cudaLaunchKernelEx(&cfg, paged_join_kernel<D, InT, HG, HW>, a, grid)) != cudaSuccess) return e;

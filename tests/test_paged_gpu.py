@@ -147,6 +147,31 @@ def test_rows_share_pages():
     _run(x)
 
 
+@pytest.mark.parametrize("new", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H,Hkv,D", [(8, 2, 128), (16, 16, 64), (7, 1, 64), (40, 1, 128), (18, 2, 64)])
+def test_a_wider_table_changes_nothing(H, Hkv, D, dtype, new):
+    # short tables: a CTA takes whole rows; wide ones: the CTAs share the keys
+    for lengths in ([40, 0, -1, 33, 1, 16], [3] * 300, [250, 249, 0, 7]):
+        x = _case(lengths, H, Hkv, D, 16, dtype, 18, new=new)
+        B, n = x["block_table"].shape
+        wide = torch.full((B, 5000), -7, dtype=torch.int32, device="cuda")
+        wide[:, :n] = x["block_table"]
+        y = dict(x, k_cache=x["k_cache"].clone(), v_cache=x["v_cache"].clone(), block_table=wide)
+        out, out2 = (torch.full((B, H, D), 5.0, device="cuda").to(x["q"].dtype) for _ in range(2))
+        before = (x["k_cache"].clone(), x["v_cache"].clone())
+        _call(x, out=out)
+        _call(y, out=out2)
+        kda.check_status()
+        _check(x, before, out)
+        _check(y, before, out2)
+        for b, m in enumerate(lengths):
+            if m < 0:
+                assert bool((out[b] == 5).all()) and bool((out2[b] == 5).all())
+            elif m == 0 and not new:
+                assert not out[b].any() and not out2[b].any()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("n", [0, 31, 64, 700])
 def test_rows_that_write_one_position_attend_to_their_own_key(n, dtype):
