@@ -73,20 +73,26 @@ __device__ __forceinline__ unsigned long long owners_of(unsigned long long total
     return total < grid ? total : grid;
 }
 
-// Block-wide: the units of all rows, and row b with its first unit: the row asked for
+// Block-wide: the units of all rows, the most tiles of any (for one `per`), and row b with its first unit: the row asked for
 // (row >= 0), or else the one that the first unit of CTA `part` of `parts` belongs to (b = B
 // if there is none).  `per` units stand beside each other for every tile of a row (heads).
-struct RowAt { int b, keys; unsigned long long first, total; };
+struct RowAt { int b, keys, most; unsigned long long first, total; };
 template <int HW>
 __device__ __forceinline__ RowAt find_row(const PagedArgs &a, unsigned long long per, unsigned long long part,
                                           unsigned long long parts, int row)
 {
     __shared__ unsigned long long s_sum[kThreads / 32], s_first;
-    __shared__ int s_b, s_keys;
+    __shared__ int s_b, s_keys, s_most[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = (a.B + kThreads - 1) / kThreads, b0 = min(tid * n, a.B), b1 = min(b0 + n, a.B);
     unsigned long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += per * (unsigned long long)tiles_of<HW>(row_keys(a, b));
+    int most = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int tiles = tiles_of<HW>(row_keys(a, b));
+        sum += per * (unsigned long long)tiles;
+        most = max(most, tiles);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
     unsigned long long inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -94,13 +100,14 @@ __device__ __forceinline__ RowAt find_row(const PagedArgs &a, unsigned long long
         if (lane >= o) inc += x;
     }
     if (tid == 0) s_b = a.B;
-    if (lane == 31) s_sum[warp] = inc;
+    if (lane == 31) { s_sum[warp] = inc; s_most[warp] = most; }
     __syncthreads();
     unsigned long long before = inc - sum, total = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += s_sum[w];
         total += s_sum[w];
+        most = max(most, s_most[w]);
     }
     // by row (row >= 0), or by the first unit of part `part` of `parts`
     const unsigned long long at = total ? part * total / owners_of(total, parts) : 0;
@@ -116,6 +123,7 @@ __device__ __forceinline__ RowAt find_row(const PagedArgs &a, unsigned long long
     r.keys = s_keys;
     r.first = s_first;
     r.total = total;
+    r.most = most;
     return r;
 }
 
@@ -155,6 +163,30 @@ struct PagedSmem {
     static constexpr int total = off_ml + kWarps * HG * 8;
     static_assert(kWarps * HG * D * 4 <= ring, "the warps' outputs meet in the ring");
 };
+
+// CTAs that fit an SM by their shared memory
+template <int D, typename InT, int HG>
+constexpr int resident() { return 226 * 1024 / (PagedSmem<D, InT, HG>::total + 1024); }
+
+// Whether it pays that CTAs take stretches of whole rows: nothing is left to join then, and no CTA
+// empties its pipeline at a row's end inside its share.  It does for many rows and for short ones; for
+// few long ones the CTAs share the keys.  With `most` units in the longest row and `units` in
+// all, the first form takes about 6 us and a unit's time for every unit of every wave of CTAs, the
+// second 12 us, its share of the units, and 14 us for every row that begins in a CTA's share.
+// In a graph, us, shared / whole (32 / 8 heads of 128 bf16, rows up to L keys, drawn):
+// 64 rows, L 250 32 / 15, L 1000 53 / 37; 128 rows, L 450 64 / 33, L 5000 259 / 270;
+// 16 rows, L 450 19 / 17, L 2500 27 / 59; one row, L 500 11.5 / 16.2.
+// (In hundredths of a us.)  `launched`: the kernel that joins has been launched, and costs 3 us even
+// if it finds nothing to do.
+template <int D, typename InT, int HG>
+__host__ __device__ __forceinline__ bool whole_rows_pay(unsigned long long stretches, unsigned long long units,
+                                                        unsigned long long most, bool launched)
+{
+    constexpr int R = resident<D, InT, HG>();
+    constexpr unsigned long long unit = R == 1 ? 160 : R == 2 ? 62 : 42, places = kSms * R;
+    return 600 + (launched ? 300 : 0) + unit * most * ((stretches + places - 1) / places) <=
+           1200 + (unit * units + 1400 * stretches) / places;
+}
 
 // The running maximum, sum and output of HG query heads over a warp's keys.  Lane's share:
 // bf16: heads 2 (lane % 4) + {0, 1} + 8 n of n-tile n; output channels lane / 4 + 8 x;
@@ -356,9 +388,16 @@ struct SimtState {
     }
 };
 
+// What the first kernel tells the second, behind the CTAs' slots in the workspace
+template <int D, int HG, int HW>
+__device__ __forceinline__ int *whole_flag(const PagedArgs &a)
+{
+    return reinterpret_cast<int *>(a.ws + (size_t)kSms * kMaxResident * 2 * HW * HG * (D + 2));
+}
+
 template <int D, typename InT, int HG, int HW>
 __global__ void __launch_bounds__(kThreads)
-paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page, const bool whole_rows)
+paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page, const bool all_whole)
 {
     using L = PagedSmem<D, InT, HG>;
     constexpr int CPR = D * (int)sizeof(InT) / 16;      // 16-byte pieces of a row
@@ -377,174 +416,183 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page, 
     const int group = a.H / a.Hkv, blocks = (group + HG - 1) / HG;
     const unsigned long long per = (unsigned long long)(a.Hkv / HW) * blocks;
     // this CTA's units [u, u1), the first of them in row b, whose own begin at row_first
-    unsigned long long u, u1, row_first;
-    int b, n, part = 0, tiles;
-    if (whole_rows) {
-        const unsigned int hb = blockIdx.x % (unsigned int)per;
-        b = blockIdx.x / (unsigned int)per;
-        n = row_keys(a, b);
-        tiles = tiles_of<HW>(n);
-        row_first = 0;
-        u = (unsigned long long)hb * tiles;
-        u1 = u + tiles;
-        if (n == 0) {                                   // no keys: zeros
-            const int blk0 = (int)(hb % blocks) * HG, nh = min(HG, group - blk0);
-            for (int e = tid; e < HW * nh * D; e += kThreads) {
-                const size_t head = (size_t)b * a.H + (hb / blocks * HW + e / (nh * D)) * group + blk0 + e / D % nh;
-                static_cast<InT *>(a.out)[head * D + e % D] = la_round<InT>(0.f);
-            }
-        }
-    } else {
+    unsigned long long u = 0, u1 = 0, row_first = 0;
+    int b = 0, n = 0, part = 0, tiles = 0;
+    const unsigned int stretches = (unsigned int)(a.B * per);
+    unsigned int next = blockIdx.x;                     // the stretch to take whole
+    bool whole_rows = all_whole;
+    if (!all_whole) {
         const RowAt at = find_row<HW>(a, per, blockIdx.x, gridDim.x, -1);
+        whole_rows = whole_rows_pay<D, InT, HG>(stretches, at.total, at.most, true);
+        if (blockIdx.x == 0 && tid == 0) *whole_flag<D, HG, HW>(a) = whole_rows;
         const unsigned long long owners = owners_of(at.total, gridDim.x);
-        if (blockIdx.x >= owners) return;
-        u = (unsigned long long)blockIdx.x * at.total / owners;
-        u1 = ((unsigned long long)blockIdx.x + 1) * at.total / owners;
-        b = at.b;
-        n = at.keys;
-        tiles = tiles_of<HW>(n);
-        row_first = at.first;
-    }
-    while (u < u1) {
-        while (u >= row_first + per * tiles) {          // next row that has units
-            row_first += per * tiles;
-            n = row_keys(a, ++b);
+        if (!whole_rows && blockIdx.x < owners) {
+            u = (unsigned long long)blockIdx.x * at.total / owners;
+            u1 = ((unsigned long long)blockIdx.x + 1) * at.total / owners;
+            b = at.b;
+            n = at.keys;
             tiles = tiles_of<HW>(n);
+            row_first = at.first;
         }
-        const int hb = (int)((u - row_first) / tiles);          // (key-value heads, block) of the stretch
-        const int hk0 = hb / blocks * HW, blk0 = (hb % blocks) * HG, nh = min(HG, group - blk0);
-        const int hk = hk0 + warp / TW;                         // this warp's
-        const int tile0 = (int)((u - row_first) % tiles);
-        const int tile1 = (int)min((unsigned long long)tiles, (unsigned long long)tile0 + (u1 - u));
-        const bool whole = tile0 == 0 && tile1 == tiles;
-        const int new_at = a.k ? n - 1 : -1;
-        const int *table = a.block_table + (size_t)b * a.max_pages;
-
-        // Page of this lane's key of a unit: key lane % 16 of the warp's 16 (-1: none).
-        auto key_of = [&](int tile) { return tile * kTile + (warp % TW) * kWarpKeys + (lane & 15); };
-        auto page_of = [&](int tile) {
-            const int t = key_of(tile);
-            return tile < tile1 && t < n ? table[quotient((unsigned int)t, by_page)] : -1;
-        };
-        // One slot of this warp's ring; rows that do not count are zeros and nothing is read for
-        // them.  Returns a bit for each key that counts.
-        auto fetch = [&](int tile, int page) {
-            const int t = key_of(tile);
-            const bool mine = tile < tile1 && t < n, is_new = mine && t == new_at;
-            const bool good = page >= 0 && page < a.num_pages;
-            if (mine && !good) atomicOr(&g_paged_status, 1u);
-            const bool real = is_new || (mine && good);
-            const InT *kp = static_cast<const InT *>(a.k_cache), *vp = static_cast<const InT *>(a.v_cache);
-            if (is_new) {
-                kp = static_cast<const InT *>(a.k) + ((size_t)b * a.Hkv + hk) * D;
-                vp = static_cast<const InT *>(a.v) + ((size_t)b * a.Hkv + hk) * D;
-            } else if (real) {
-                const size_t off = (((size_t)page * a.page_size + ((unsigned int)t - quotient((unsigned int)t, by_page) * by_page.d)) *
-                                        a.Hkv + hk) * D;
-                kp += off;
-                vp += off;
-            }
-            const unsigned int seen = __ballot_sync(0xffffffffu, real) & 0xffffu;
-            const uint32_t dst = ring + (uint32_t)((tile % kStages) * L::slot + (lane / CPR) * L::row + 16 * (lane % CPR));
-            const unsigned long long kpi = reinterpret_cast<unsigned long long>(kp) , vpi = reinterpret_cast<unsigned long long>(vp);
-#pragma unroll
-            for (int e = 0; e < kWarpKeys / RPI; ++e) {
-                const int r = e * RPI + lane / CPR;
-                const bool ok = (seen >> r) & 1u;
-                const unsigned long long ks = __shfl_sync(0xffffffffu, kpi, r), vs = __shfl_sync(0xffffffffu, vpi, r);
-                cp16(dst + (uint32_t)(e * RPI * L::row), reinterpret_cast<const uint8_t *>(ks) + 16 * (lane % CPR), ok);
-                cp16(dst + (uint32_t)((kWarpKeys + e * RPI) * L::row), reinterpret_cast<const uint8_t *>(vs) + 16 * (lane % CPR), ok);
-            }
-            cp_commit();
-            return seen;
-        };
-
-        static_assert(kStages == 3, "two units ahead");
-        unsigned int seen0 = fetch(tile0, page_of(tile0)), seen1 = fetch(tile0 + 1, page_of(tile0 + 1)), seen2;
-        int page2 = page_of(tile0 + 2);
-        const InT *qh = static_cast<const InT *>(a.q) + ((size_t)b * a.H + hk * group + blk0) * D;
-        if constexpr (L::mma) {
-            MmaState<D, HG> st;
-            st.start(qh, nh, lane);
-            for (int tile = tile0; tile < tile1; ++tile) {
-                seen2 = fetch(tile + 2, page2);
-                page2 = page_of(tile + 3);
-                cp_wait<2>();
-                __syncwarp();
-                const uint32_t k = ring + (uint32_t)((tile % kStages) * L::slot);
-                st.step(k, k + kWarpKeys * L::row, L::row, seen0, a.scale * kLog2e, lane);
-                seen0 = seen1;
-                seen1 = seen2;
-                __syncwarp();                           // the slot is free again
-            }
-            cp_wait<0>();
-            __syncthreads();
-            st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
-        } else {
-            float *sQ = reinterpret_cast<float *>(smem + L::off_q) + warp * HG * D;
-            float *sP = reinterpret_cast<float *>(smem + L::off_p) + warp * HG * kWarpKeys;
-            for (int e = lane; e < HG * D; e += 32) sQ[e] = e / D < nh ? to_f32(qh[e]) * (a.scale * kLog2e) : 0.f;
-            __syncwarp();
-            SimtState<D, HG> st;
-            st.start();
-            for (int tile = tile0; tile < tile1; ++tile) {
-                seen2 = fetch(tile + 2, page2);
-                page2 = page_of(tile + 3);
-                cp_wait<2>();
-                __syncwarp();
-                const uint8_t *k = smem + (warp * kStages + tile % kStages) * L::slot;
-                st.step(k, k + kWarpKeys * L::row, L::row, seen0, sQ, sP, lane);
-                seen0 = seen1;
-                seen1 = seen2;
-                __syncwarp();                           // the slot and sP are free again
-            }
-            cp_wait<0>();
-            __syncthreads();
-            st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
-        }
-        // ---- the new token's keys and values go to their place in the cache (one owner per head)
-        if (new_at >= 0 && blk0 == 0 && new_at / kTile >= tile0 && new_at / kTile < tile1) {
-            const unsigned int pi = quotient((unsigned int)new_at, by_page);
-            const int page = table[pi];
-            if (page >= 0 && page < a.num_pages) {
-                const size_t dst = (((size_t)page * a.page_size + ((unsigned int)new_at - pi * by_page.d)) * a.Hkv + hk0) * D;
-                const size_t src = ((size_t)b * a.Hkv + hk0) * D;
-                for (int e = tid; e < HW * CPR; e += kThreads) {
-                    reinterpret_cast<uint4 *>(static_cast<InT *>(a.k_cache) + dst)[e] =
-                        reinterpret_cast<const uint4 *>(static_cast<const InT *>(a.k) + src)[e];
-                    reinterpret_cast<uint4 *>(static_cast<InT *>(a.v_cache) + dst)[e] =
-                        reinterpret_cast<const uint4 *>(static_cast<const InT *>(a.v) + src)[e];
+    }
+    do {
+        if (whole_rows && next < stretches) {
+            const unsigned int hb = next % (unsigned int)per;
+            b = next / (unsigned int)per;
+            n = row_keys(a, b);
+            tiles = tiles_of<HW>(n);
+            u = (unsigned long long)hb * tiles;
+            u1 = u + tiles;
+            if (n == 0) {                                   // no keys: zeros
+                const int blk0 = (int)(hb % blocks) * HG, nh = min(HG, group - blk0);
+                for (int e = tid; e < HW * nh * D; e += kThreads) {
+                    const size_t head = (size_t)b * a.H + (hb / blocks * HW + e / (nh * D)) * group + blk0 + e / D % nh;
+                    static_cast<InT *>(a.out)[head * D + e % D] = la_round<InT>(0.f);
                 }
             }
+            next += gridDim.x;
         }
-        // ---- the warps of a head meet
-        __syncthreads();
-        float *slot = a.ws + ((size_t)blockIdx.x * 2 + (part > 0 ? 1 : 0)) * HW * HG * (D + 2);
-        for (int e = tid; e < HW * nh * D; e += kThreads) {
-            const int hw = e / (nh * D), g = e / D % nh, d = e % D;
-            float top = -INFINITY, sum = 0.f, acc = 0.f;
-#pragma unroll
-            for (int w = 0; w < TW; ++w) top = fmaxf(top, sML[((hw * TW + w) * HG + g) * 2]);
-#pragma unroll
-            for (int w = 0; w < TW; ++w) {
-                const int x = (hw * TW + w) * HG + g;
-                const float mw = sML[x * 2], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
-                sum += f * sML[x * 2 + 1];
-                acc += f * sO[x * D + d];
+        while (u < u1) {
+            while (u >= row_first + per * tiles) {          // next row that has units
+                row_first += per * tiles;
+                n = row_keys(a, ++b);
+                tiles = tiles_of<HW>(n);
             }
-            if (whole) {
-                static_cast<InT *>(a.out)[((size_t)b * a.H + (hk0 + hw) * group + blk0 + g) * D + d] =
-                    la_round<InT>(sum > 0.f ? acc / sum : 0.f);
+            const int hb = (int)((u - row_first) / tiles);          // (key-value heads, block) of the stretch
+            const int hk0 = hb / blocks * HW, blk0 = (hb % blocks) * HG, nh = min(HG, group - blk0);
+            const int hk = hk0 + warp / TW;                         // this warp's
+            const int tile0 = (int)((u - row_first) % tiles);
+            const int tile1 = (int)min((unsigned long long)tiles, (unsigned long long)tile0 + (u1 - u));
+            const bool whole = tile0 == 0 && tile1 == tiles;
+            const int new_at = a.k ? n - 1 : -1;
+            const int *table = a.block_table + (size_t)b * a.max_pages;
+
+            // Page of this lane's key of a unit: key lane % 16 of the warp's 16 (-1: none).
+            auto key_of = [&](int tile) { return tile * kTile + (warp % TW) * kWarpKeys + (lane & 15); };
+            auto page_of = [&](int tile) {
+                const int t = key_of(tile);
+                return tile < tile1 && t < n ? table[quotient((unsigned int)t, by_page)] : -1;
+            };
+            // One slot of this warp's ring; rows that do not count are zeros and nothing is read for
+            // them.  Returns a bit for each key that counts.
+            auto fetch = [&](int tile, int page) {
+                const int t = key_of(tile);
+                const bool mine = tile < tile1 && t < n, is_new = mine && t == new_at;
+                const bool good = page >= 0 && page < a.num_pages;
+                if (mine && !good) atomicOr(&g_paged_status, 1u);
+                const bool real = is_new || (mine && good);
+                const InT *kp = static_cast<const InT *>(a.k_cache), *vp = static_cast<const InT *>(a.v_cache);
+                if (is_new) {
+                    kp = static_cast<const InT *>(a.k) + ((size_t)b * a.Hkv + hk) * D;
+                    vp = static_cast<const InT *>(a.v) + ((size_t)b * a.Hkv + hk) * D;
+                } else if (real) {
+                    const size_t off = (((size_t)page * a.page_size + ((unsigned int)t - quotient((unsigned int)t, by_page) * by_page.d)) *
+                                            a.Hkv + hk) * D;
+                    kp += off;
+                    vp += off;
+                }
+                const unsigned int seen = __ballot_sync(0xffffffffu, real) & 0xffffu;
+                const uint32_t dst = ring + (uint32_t)((tile % kStages) * L::slot + (lane / CPR) * L::row + 16 * (lane % CPR));
+                const unsigned long long kpi = reinterpret_cast<unsigned long long>(kp) , vpi = reinterpret_cast<unsigned long long>(vp);
+#pragma unroll
+                for (int e = 0; e < kWarpKeys / RPI; ++e) {
+                    const int r = e * RPI + lane / CPR;
+                    const bool ok = (seen >> r) & 1u;
+                    const unsigned long long ks = __shfl_sync(0xffffffffu, kpi, r), vs = __shfl_sync(0xffffffffu, vpi, r);
+                    cp16(dst + (uint32_t)(e * RPI * L::row), reinterpret_cast<const uint8_t *>(ks) + 16 * (lane % CPR), ok);
+                    cp16(dst + (uint32_t)((kWarpKeys + e * RPI) * L::row), reinterpret_cast<const uint8_t *>(vs) + 16 * (lane % CPR), ok);
+                }
+                cp_commit();
+                return seen;
+            };
+
+            static_assert(kStages == 3, "two units ahead");
+            unsigned int seen0 = fetch(tile0, page_of(tile0)), seen1 = fetch(tile0 + 1, page_of(tile0 + 1)), seen2;
+            int page2 = page_of(tile0 + 2);
+            const InT *qh = static_cast<const InT *>(a.q) + ((size_t)b * a.H + hk * group + blk0) * D;
+            if constexpr (L::mma) {
+                MmaState<D, HG> st;
+                st.start(qh, nh, lane);
+                for (int tile = tile0; tile < tile1; ++tile) {
+                    seen2 = fetch(tile + 2, page2);
+                    page2 = page_of(tile + 3);
+                    cp_wait<2>();
+                    __syncwarp();
+                    const uint32_t k = ring + (uint32_t)((tile % kStages) * L::slot);
+                    st.step(k, k + kWarpKeys * L::row, L::row, seen0, a.scale * kLog2e, lane);
+                    seen0 = seen1;
+                    seen1 = seen2;
+                    __syncwarp();                           // the slot is free again
+                }
+                cp_wait<0>();
+                __syncthreads();
+                st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
             } else {
-                float *mine = slot + hw * HG * (D + 2);
-                mine[g * D + d] = acc;
-                if (d == 0) { mine[HG * D + 2 * g] = top; mine[HG * D + 2 * g + 1] = sum; }
+                float *sQ = reinterpret_cast<float *>(smem + L::off_q) + warp * HG * D;
+                float *sP = reinterpret_cast<float *>(smem + L::off_p) + warp * HG * kWarpKeys;
+                for (int e = lane; e < HG * D; e += 32) sQ[e] = e / D < nh ? to_f32(qh[e]) * (a.scale * kLog2e) : 0.f;
+                __syncwarp();
+                SimtState<D, HG> st;
+                st.start();
+                for (int tile = tile0; tile < tile1; ++tile) {
+                    seen2 = fetch(tile + 2, page2);
+                    page2 = page_of(tile + 3);
+                    cp_wait<2>();
+                    __syncwarp();
+                    const uint8_t *k = smem + (warp * kStages + tile % kStages) * L::slot;
+                    st.step(k, k + kWarpKeys * L::row, L::row, seen0, sQ, sP, lane);
+                    seen0 = seen1;
+                    seen1 = seen2;
+                    __syncwarp();                           // the slot and sP are free again
+                }
+                cp_wait<0>();
+                __syncthreads();
+                st.finish(sO + warp * HG * D, sML + warp * HG * 2, lane);
             }
+            // ---- the new token's keys and values go to their place in the cache (one owner per head)
+            if (new_at >= 0 && blk0 == 0 && new_at / kTile >= tile0 && new_at / kTile < tile1) {
+                const unsigned int pi = quotient((unsigned int)new_at, by_page);
+                const int page = table[pi];
+                if (page >= 0 && page < a.num_pages) {
+                    const size_t dst = (((size_t)page * a.page_size + ((unsigned int)new_at - pi * by_page.d)) * a.Hkv + hk0) * D;
+                    const size_t src = ((size_t)b * a.Hkv + hk0) * D;
+                    for (int e = tid; e < HW * CPR; e += kThreads) {
+                        reinterpret_cast<uint4 *>(static_cast<InT *>(a.k_cache) + dst)[e] =
+                            reinterpret_cast<const uint4 *>(static_cast<const InT *>(a.k) + src)[e];
+                        reinterpret_cast<uint4 *>(static_cast<InT *>(a.v_cache) + dst)[e] =
+                            reinterpret_cast<const uint4 *>(static_cast<const InT *>(a.v) + src)[e];
+                    }
+                }
+            }
+            // ---- the warps of a head meet
+            __syncthreads();
+            float *slot = a.ws + ((size_t)blockIdx.x * 2 + (part > 0 ? 1 : 0)) * HW * HG * (D + 2);
+            for (int e = tid; e < HW * nh * D; e += kThreads) {
+                const int hw = e / (nh * D), g = e / D % nh, d = e % D;
+                float top = -INFINITY, sum = 0.f, acc = 0.f;
+#pragma unroll
+                for (int w = 0; w < TW; ++w) top = fmaxf(top, sML[((hw * TW + w) * HG + g) * 2]);
+#pragma unroll
+                for (int w = 0; w < TW; ++w) {
+                    const int x = (hw * TW + w) * HG + g;
+                    const float mw = sML[x * 2], f = mw == -INFINITY ? 0.f : exp2f(mw - top);
+                    sum += f * sML[x * 2 + 1];
+                    acc += f * sO[x * D + d];
+                }
+                if (whole) {
+                    static_cast<InT *>(a.out)[((size_t)b * a.H + (hk0 + hw) * group + blk0 + g) * D + d] =
+                        la_round<InT>(sum > 0.f ? acc / sum : 0.f);
+                } else {
+                    float *mine = slot + hw * HG * (D + 2);
+                    mine[g * D + d] = acc;
+                    if (d == 0) { mine[HG * D + 2 * g] = top; mine[HG * D + 2 * g + 1] = sum; }
+                }
+            }
+            __syncthreads();                                // sO and sML lie where the next stretch's copies go
+            u += (unsigned long long)(tile1 - tile0);
+            ++part;
         }
-        __syncthreads();                                // sO and sML lie where the next stretch's copies go
-        u += (unsigned long long)(tile1 - tile0);
-        ++part;
-    }
+    } while (whole_rows && next < stretches);
 }
 
 // One CTA per (row, query head): rows without keys get zeros, and stretches that several CTAs
@@ -560,6 +608,7 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (*whole_flag<D, HG, HW>(a)) return;              // every row has been written out
     const int n = row_keys(a, b);
     if (n < 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -638,28 +687,6 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
     }
 }
 
-// CTAs that fit an SM by their shared memory
-template <int D, typename InT, int HG>
-constexpr int resident() { return 226 * 1024 / (PagedSmem<D, InT, HG>::total + 1024); }
-
-// Whether each CTA takes one row whole (for its heads): nothing is left to join then, and no CTA
-// empties its pipeline at a row's end to fill it again.  It pays for many rows and for short ones;
-// for few long ones the CTAs share the keys.  What the host knows are the table's bounds: with
-// `most` units to a row the first form takes about 6 us and a unit's time for every unit of every
-// wave of CTAs, the second 12 us, its share of the units, and 14 us for every row that begins in
-// a CTA's share.  In a graph, us, shared / whole (32 / 8 heads of 128 bf16, rows up to L keys, drawn):
-// 64 rows, L 250 32 / 15, L 1000 53 / 37; 128 rows, L 450 64 / 33, L 5000 259 / 270;
-// 16 rows, L 450 19 / 17, L 2500 27 / 59; one row, L 500 11.5 / 16.2.
-template <int D, typename InT, int HG, int HW>
-bool takes_whole_rows(const PagedArgs &a)
-{
-    constexpr int R = resident<D, InT, HG>();
-    constexpr double unit = R == 1 ? 1.6 : R == 2 ? 0.62 : 0.42;       // us, with R CTAs on an SM
-    const double stretches = (double)a.B * (a.Hkv / HW) * ((a.H / a.Hkv + HG - 1) / HG), share = stretches / (kSms * R);
-    const double most = ceil((double)a.max_pages * a.page_size / unit_keys<HW>());
-    return 6 + unit * most * ceil(share) <= 12 + (unit * most + 14) * share;
-}
-
 // Query heads that share one reading of the cache.  bf16: 8 columns of a product, or two
 // times 8 for larger groups (a third would no longer fit the registers); fp32: as many as the
 // group has, up to 8.
@@ -685,8 +712,11 @@ cudaError_t launch_typed(const PagedArgs &a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     static_assert(resident<D, InT, HG>() <= kMaxResident, "the workspace holds two stretches per CTA");
     unsigned int grid = kSms * resident<D, InT, HG>();
-    const bool whole_rows = takes_whole_rows<D, InT, HG, HW>(a);
-    if (whole_rows) grid = (unsigned int)((size_t)a.B * (a.Hkv / HW) * ((a.H / a.Hkv + HG - 1) / HG));
+    // by the table's bounds, which are what the host knows; otherwise the device decides by the lengths
+    const unsigned long long stretches = (unsigned long long)a.B * (a.Hkv / HW) * ((a.H / a.Hkv + HG - 1) / HG);
+    const unsigned long long most = ((unsigned long long)a.max_pages * a.page_size + unit_keys<HW>() - 1) / unit_keys<HW>();
+    const bool whole_rows = whole_rows_pay<D, InT, HG>(stretches, stretches * most, most, false);
+    if (whole_rows) grid = (unsigned int)stretches;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
@@ -731,7 +761,7 @@ cudaError_t launch_group(const PagedArgs &a, cudaStream_t stream)
 
 size_t paged_workspace_bytes(int H, int Hkv, int D, kda_dtype dtype)
 {
-    return sizeof(float) * (size_t)kSms * kMaxResident * 2 * heads_per_unit(Hkv) * heads_per_block(H / Hkv, dtype) * (D + 2);
+    return sizeof(float) * (size_t)kSms * kMaxResident * 2 * heads_per_unit(Hkv) * heads_per_block(H / Hkv, dtype) * (D + 2) + 256;
 }
 
 cudaError_t launch_paged_decode(const PagedArgs &a, cudaStream_t stream)

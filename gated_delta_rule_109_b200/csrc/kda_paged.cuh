@@ -16,8 +16,8 @@
 // one owner is written out at once; one that several CTAs share leaves each owner's running
 // maximum, sum and unnormalised output in the workspace, and a second kernel joins them.
 // The lengths are read on the device: nothing of that split depends on what the host knows.
-// Where the table has room for short rows only, or there are many, every row has one owner for each
-// group of heads and block instead, and there is no second kernel.
+// Where the rows are short, or many, every row has one owner for each group of heads and block
+// instead; if already the table's bounds tell that, there is no second kernel.
 #pragma once
 
 #include "kda_internal.cuh"
