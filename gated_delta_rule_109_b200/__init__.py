@@ -599,24 +599,38 @@ def _address(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _with_scratch(nbytes: int, index: int, fn, *args) -> int:
+    """fn(*args, scratch, its bytes, current stream), the scratch from torch's allocator for the
+    stream: given back as soon as the call is enqueued, to whatever the stream does next."""
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _with_scratch(nbytes, index, fn, *args)
+    stream = _raw_stream(index)
+    scratch = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+    try:
+        return fn(*args, scratch, nbytes, stream)
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(scratch)
+
+
 @functools.lru_cache(maxsize=256)
 def _size(name, *sizes) -> int:
     """A workspace's bytes from the library, which depend on nothing but these sizes."""
     return getattr(load(), name)(*sizes)
 
 
-def _la_workspace(q, dk, dv, code, workspace, where):
-    """Address and bytes of a linear-attention call's workspace, and the tensor: the caller's,
-    or a new one where the sizes need any (from torch's allocator, on the current stream)."""
-    B, T, H = q.shape[:3]
+def _la_run(name, q, dk, dv, code, workspace, *args):
+    """The linear-attention call `name`, with the caller's workspace or, where the sizes need any,
+    with scratch of its own."""
+    index, fn = q.get_device(), getattr(load(), name)
     if workspace is None:
-        n = _size(where + "_workspace_bytes", B, T, H, dk, dv, code)
-        if not n:
-            return None, 0, None
-        workspace = q.new_empty(n, dtype=torch.uint8)
-        return workspace.data_ptr(), n, workspace
-    _need_workspace(workspace, q.device, where)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+        n = _size(name + "_workspace_bytes", *q.shape[:3], dk, dv, code)
+        st = _with_scratch(n, index, fn, *args) if n else _launch(index, fn, *args, None, 0)
+    else:
+        _need_workspace(workspace, q.device, name)
+        st = _launch(index, fn, *args, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if st:
+        _check(st, name)
 
 
 def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, backward=False) -> int:
@@ -674,11 +688,8 @@ def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=
         out = torch.empty_like(v)
     if final_state is None and return_final_state:
         final_state = q.new_empty(state, dtype=torch.float32) if initial_state is None else torch.empty_like(initial_state)
-    ws, nbytes, _hold = _la_workspace(q, dk, dv, code, workspace, "kda_la_forward")
-    st = _launch(q.get_device(), lib.kda_la_forward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
-                 _address(initial_state), out.data_ptr(), _address(final_state), B, T, H, dk, dv, code, scale, ws, nbytes)
-    if st:
-        _check(st, "kda_la_forward")
+    _la_run("kda_la_forward", q, dk, dv, code, workspace, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
+            _address(initial_state), out.data_ptr(), _address(final_state), B, T, H, dk, dv, code, scale)
     return out, final_state
 
 
@@ -700,12 +711,9 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
                     (grad_final_state, "grad_final_state", state, torch.float32))
     dq, dkey, dval = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds0 = q.new_empty(state, dtype=torch.float32) if initial_state_grad else None
-    ws, nbytes, _hold = _la_workspace(q, dk, dv, code, workspace, "kda_la_backward")
-    st = _launch(q.get_device(), lib.kda_la_backward, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
-                 _address(initial_state), grad_out.data_ptr(), _address(grad_final_state), dq.data_ptr(),
-                 dkey.data_ptr(), dval.data_ptr(), _address(ds0), B, T, H, dk, dv, code, scale, ws, nbytes)
-    if st:
-        _check(st, "kda_la_backward")
+    _la_run("kda_la_backward", q, dk, dv, code, workspace, q.data_ptr(), k.data_ptr(), v.data_ptr(), _address(log_decay),
+            _address(initial_state), grad_out.data_ptr(), _address(grad_final_state), dq.data_ptr(), dkey.data_ptr(),
+            dval.data_ptr(), _address(ds0), B, T, H, dk, dv, code, scale)
     return dict(dq=dq, dk=dkey, dv=dval, dinitial_state=ds0)
 
 
@@ -796,15 +804,17 @@ def paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths, *, out=No
                 _need(t, name, want, d, q.device)
     if out is None:
         out = torch.empty_like(q)
+    args = (q.data_ptr(), _address(k), _address(v), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+            lengths.data_ptr(), out.data_ptr(), B, H, Hkv, D, num_pages, page_size, max_pages, code, scale)
     if workspace is None:
         nbytes = _size("kda_paged_decode_workspace_bytes", H, Hkv, D, code)
-        workspace = q.new_empty(nbytes, dtype=torch.uint8)
+        if not nbytes:                                  # sizes that the call refuses
+            nbytes = 256
+        st = _with_scratch(nbytes, index, lib.kda_paged_decode_step, *args)
     else:
         _need_workspace(workspace, q.device, "kda_paged_decode_step")
-        nbytes = workspace.numel() * workspace.element_size()
-    st = _launch(index, lib.kda_paged_decode_step, q.data_ptr(), _address(k), _address(v), k_cache.data_ptr(),
-                 v_cache.data_ptr(), block_table.data_ptr(), lengths.data_ptr(), out.data_ptr(), B, H, Hkv, D, num_pages,
-                 page_size, max_pages, code, scale, workspace.data_ptr(), nbytes)
+        st = _launch(index, lib.kda_paged_decode_step, *args, workspace.data_ptr(),
+                     workspace.numel() * workspace.element_size())
     if st:
         _check(st, "kda_paged_decode_step")
     return out
