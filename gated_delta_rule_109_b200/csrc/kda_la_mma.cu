@@ -11,6 +11,8 @@
 // barriers'.  A chunk's loads are all under way together, ahead of the state's update, and
 // two CTAs share an SM where they fit.  Powers of lambda are computed in 64 bits once per CTA,
 // so their rounding does not grow along the sequence.
+#include <type_traits>
+
 #include "kda_la.cuh"
 
 namespace kda {
@@ -242,44 +244,35 @@ la_mma_kernel(const __grid_constant__ LaArgs a)
         __syncthreads();                        // the chunk's rows and the state are there
 
         if (!STATES_ONLY) {
-            // ---- P_ij = f_intra lambda^(i-j) (q_i . k_j), j <= i.  Tiles that no pair j <= i falls
-            // into are left out, here and in P V.
-            if (2 * wc <= wr) {
-                float s[4][4] = {};
+            // ---- P_ij = f_intra lambda^(i-j) (q_i . k_j), j <= i: of the 2 (wr + 1) tiles of 8 columns
+            // that hold such pairs each of a row's two warps makes half
+            auto scores = [&](auto tiles) {
+                constexpr int N = decltype(tiles)::value;
+                const int first = 8 * N * wc;
+                float s[N][4] = {};
 #pragma unroll 2
                 for (int d = t2; d < DK; d += 8) {
-                    float2 y[4];
+                    float2 y[N];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) y[n] = load2(sK + (col + 8 * n + g) * PK + d);
+                    for (int n = 0; n < N; ++n) y[n] = load2(sK + (first + 8 * n + g) * PK + d);
                     mma_split<EX, EX, EX>(s, load2(sQ + row * PK + d), load2(sQ + (row + 8) * PK + d), y);
                 }
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < N; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int r = row + 8 * i, m = col + 8 * n + t2, apart = r - m;
+                        const int r = row + 8 * i, m = first + 8 * n + t2, apart = r - m;
                         *reinterpret_cast<float2 *>(sP + r * PP + m) =
                             make_float2(apart >= 0 ? s[n][2 * i] * (sW[max(apart, 0)] * ps.f_intra) : 0.f,
                                         apart >= 1 ? s[n][2 * i + 1] * (sW[max(apart - 1, 0)] * ps.f_intra) : 0.f);
                     }
-            }
-            __syncthreads();
-            // ---- out: P V + (f_inter lambda^(.) Q) S
+            };
+            if (wr == 0) scores(std::integral_constant<int, 1>{});
+            else if (wr == 1) scores(std::integral_constant<int, 2>{});
+            else if (wr == 2) scores(std::integral_constant<int, 3>{});
+            else scores(std::integral_constant<int, 4>{});
+            // ---- out: (f_inter lambda^(.) Q) S, and with all scores there P V
             float o[4 * CV][4] = {};
-#pragma unroll 2
-            for (int j = t2; j < 16 * wr + 16; j += 8) {
-                const float2 x0 = load2(sP + row * PP + j), x1 = load2(sP + (row + 8) * PP + j);
-#pragma unroll
-                for (int m = 0; m < CV; ++m) {
-                    float2 y[4];
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const float *p = sV + j * PV + col + 64 * m + 8 * n + g;
-                        y[n] = make_float2(p[0], p[PV]);
-                    }
-                    mma_split<false, EX, EX>(o + 4 * m, x0, x1, y);
-                }
-            }
             const float f0 = ps.f_inter * sW[rev ? row : row + 1], f1 = ps.f_inter * sW[rev ? row + 8 : row + 9];
 #pragma unroll (CV > 1 ? 1 : 2)
             for (int d = t2; d < DK; d += 8) {
@@ -294,6 +287,21 @@ la_mma_kernel(const __grid_constant__ LaArgs a)
                         y[n] = make_float2(p[0], p[PV]);
                     }
                     mma_split<false, false, EX>(o + 4 * m, x0, x1, y);
+                }
+            }
+            __syncthreads();
+#pragma unroll 2
+            for (int j = t2; j < 16 * wr + 16; j += 8) {
+                const float2 x0 = load2(sP + row * PP + j), x1 = load2(sP + (row + 8) * PP + j);
+#pragma unroll
+                for (int m = 0; m < CV; ++m) {
+                    float2 y[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float *p = sV + j * PV + col + 64 * m + 8 * n + g;
+                        y[n] = make_float2(p[0], p[PV]);
+                    }
+                    mma_split<false, EX, EX>(o + 4 * m, x0, x1, y);
                 }
             }
             InT *out = static_cast<InT *>(ps.out);
