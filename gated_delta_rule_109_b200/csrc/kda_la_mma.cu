@@ -7,7 +7,7 @@
 // memory and go in as two tf32 parts, so the sums keep fp32's accuracy.  Multiply-adds on CUDA
 // cores with 4 x 4 register tiles were bound by shared memory, 3 wavefronts to 4 x 32
 // multiply-adds of a 16-byte read (B4 T2048 H32 d128 fp32 695 us, B8 T2048 H32 d64 bf16 468):
-// here they are 528 and 271, the tensor pipe is half busy and the waits are its own and the
+// here they are 504 and 266, the tensor pipe is half busy and the waits are its own and the
 // barriers'.  A chunk's loads are all under way together, ahead of the state's update, and
 // two CTAs share an SM where they fit.  Powers of lambda are computed in 64 bits once per CTA,
 // so their rounding does not grow along the sequence.
@@ -44,7 +44,7 @@ __device__ __forceinline__ void fma4(float4 &acc, float a, float4 b)
 // operand goes in as two tf32 parts of 11 bits: hi is the nearest, lo the rest with its last bits
 // cut off, 2^-22 of x at most and of either sign.  Of the four products of parts lo lo is left
 // out, 2^-22 of a term.  A NaN stays one: where the sum that rounds hi runs over, lo is the NaN.
-// (Rounding lo as well, by conversion instructions, left the same errors: 23.7 us for 22.8 at
+// (Rounding lo as well, by conversion instructions, left the same errors: 4 % more time at
 // B2 T1023 H8 d64.)  What is bf16 is its own hi.
 //
 // Lane (g, t) = (lane / 4, lane % 4) holds rows g, g + 8 of A, column g of B, and of both the
