@@ -581,7 +581,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a, const Divider by_page, 
                 }
                 if (whole) {
                     static_cast<InT *>(a.out)[((size_t)b * a.H + (hk0 + hw) * group + blk0 + g) * D + d] =
-                        la_round<InT>(sum > 0.f ? acc / sum : 0.f);
+                        la_round<InT>(sum == 0.f ? 0.f : acc / sum);     // no weight: zeros; a NaN stays one
                 } else {
                     float *mine = slot + hw * HG * (D + 2);
                     mine[g * D + d] = acc;
@@ -683,7 +683,7 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
             s += s_sum[w];
             o += s_acc[w][tid];
         }
-        out[tid] = la_round<InT>(s > 0.f ? o / s : 0.f);
+        out[tid] = la_round<InT>(s == 0.f ? 0.f : o / s);     // as above
     }
 }
 

@@ -567,7 +567,9 @@ kda_status kda_la_decode_step(const void *q, const void *k, const void *v, const
  *                 to be used by another call that may run at the same time
  *
  * A row with lengths[b] < 0 is idle: its cache and its row of out are left as they were.  A
- * row without keys (k = v = NULL, lengths[b] = 0) gets zeros.  Rows may share pages; each
+ * row without keys (k = v = NULL, lengths[b] = 0) gets zeros, and so does one whose keys all
+ * score -inf.  Infinities and NaN among what a row attends to are as in the formula: a NaN or
+ * +inf score makes the head's out NaN.  Rows may share pages; each
  * attends to its own new key, which is taken from k and v.  The position that a row writes
  * must not be one that another row reads from the cache (t < lengths[b]); where two rows
  * write the same position, it holds elements of either afterwards.
