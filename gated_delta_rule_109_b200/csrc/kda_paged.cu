@@ -12,7 +12,10 @@
 // O^T = V^T P^T, so that the 8 columns are query heads and a group of fewer than 8 wastes
 // little (with the heads as rows it would be 16).  There is one query per sequence: at most
 // some 40 flops per byte, far from what tcgen05's 128-row tiles are for.  P is split into two
-// bf16 parts, which leaves the rounding of the output as the only one of that size.
+// bf16 parts, which leaves the rounding of the output as the only one of that size.  Both parts of
+// a weight are positive (the first is the largest bf16 below it, together they are off by at most
+// 2^-16 of it), so that an infinite value stays one: rounded to nearest, the second part would be
+// zero or negative for half of all weights, and 0 or -1 times infinity a NaN.
 // fp32: CUDA cores.  Scores: lane = (key, half of the channels), the query broadcast from
 // shared memory.  Output: lane = D / 32 channels, the probabilities broadcast.
 // Sums and statistics are fp32 in both.
@@ -256,10 +259,11 @@ struct MmaState {
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(p[2 * x], p[2 * x + 1]);
-                const float2 f = __bfloat1622float2(h);
-                const __nv_bfloat162 r = __floats2bfloat162_rn(p[2 * x] - f.x, p[2 * x + 1] - f.y);
-                hi[n][x] = transpose8x8(*reinterpret_cast<const uint32_t *>(&h));
+                const float p0 = p[2 * x], p1 = p[2 * x + 1];
+                const uint32_t h0 = (__float_as_uint(p0) - (p0 > 0.f ? 1u : 0u)) & 0xffff0000u;
+                const uint32_t h1 = (__float_as_uint(p1) - (p1 > 0.f ? 1u : 0u)) & 0xffff0000u;
+                const __nv_bfloat162 r = __floats2bfloat162_rn(p0 - __uint_as_float(h0), p1 - __uint_as_float(h1));
+                hi[n][x] = transpose8x8(__byte_perm(h0, h1, 0x7632));
                 lo[n][x] = transpose8x8(*reinterpret_cast<const uint32_t *>(&r));
             }
         }
@@ -668,7 +672,8 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float f = c + i * kWarps < count ? s_weight[c + i * kWarps] : 0.f;
+            if (c + i * kWarps >= count) break;         // what was loaded there is another share's
+            const float f = s_weight[c + i * kWarps];
 #pragma unroll
             for (int y = 0; y < DL; ++y) acc[y] += f * x[i][y];
         }

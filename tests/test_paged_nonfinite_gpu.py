@@ -104,3 +104,34 @@ def test_keys_that_all_score_minus_infinity_weigh_nothing(dtype, lengths, spare)
     got = kda.paged_decode_step(*a)
     kda.check_status()
     assert not got[:, :4].any() and bool(torch.isfinite(got).all()) and bool((got[:, 4:] != 0).any())
+
+
+@pytest.mark.parametrize("lengths,spare", LAYOUTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_values_that_are_not_finite_stay_what_they_are(dtype, D, lengths, spare):
+    n = lengths[0]
+    for t in (0, 17, n // 2, n - 1):
+        x = _case(lengths, spare, dtype, D, 5)
+        x["q"] = 0.25 * x["q"]                              # weights that fp32 holds for every key
+        page, entry = _at(x, 0, t)
+        x["v_cache"][page, entry, 1, 3] = INF
+        x["v_cache"][page, entry, 1, 4] = -INF
+        x["v_cache"][page, entry, 1, 5] = NAN
+        x["v"][0, 0, 6] = -INF
+        want = _check(x)
+        assert bool((want[0, 4:, 3] == INF).all()) and bool((want[0, 4:, 4] == -INF).all())
+        assert bool(torch.isnan(want[0, 4:, 5]).all()) and bool((want[0, :4, 6] == -INF).all())
+        assert int(torch.isfinite(want[0]).sum()) == 8 * D - 16
+    x = _case(lengths, spare, dtype, D, 6)                  # +inf and -inf in one channel
+    x["q"] = 0.25 * x["q"]
+    x["v_cache"][(*_at(x, 0, 1), 0, 2)], x["v"][0, 0, 2] = INF, -INF
+    assert bool(torch.isnan(_check(x)[0, :4, 2]).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_only_key_with_an_infinite_value(dtype):
+    # its probability is 1, which one bf16 holds: nothing is left for a second part
+    x = _case([0, 0], 0, dtype, 64, 7)
+    x["v"][0, 0, 2] = INF
+    assert bool((_check(x)[0, :4, 2] == INF).all())
