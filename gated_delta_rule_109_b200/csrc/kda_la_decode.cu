@@ -12,6 +12,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// lambda as the sum of two floats.  The state of a slowly decaying head holds thousands of steps,
+// and each would repeat the rounding of a single one: 2^-25 of the state and step.  1 + expm1(g)
+// is off by 2^-23 of |g| instead, and a head remembers 1 / |g| steps.  A head that decays faster
+// than that holds a few, for which expf does.
+__device__ __forceinline__ float2 decay_of(const float *__restrict__ log_decay, int h)
+{
+    const float g = log_decay ? log_decay[h] : 0.f;
+    if (!(fabsf(g) < 0.5f)) return make_float2(expf(g), 0.f);
+    const float e = expm1f(g), hi = 1.f + e;
+    return make_float2(hi, e - (hi - 1.f));
+}
+
 template <int DK, int DV, typename InT, int NS>
 __global__ void __launch_bounds__(kThreads, 3)
 la_decode_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const InT *__restrict__ v,
@@ -36,15 +48,15 @@ la_decode_kernel(const InT *__restrict__ q, const InT *__restrict__ k, const InT
     float4 s[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) s[i] = __ldcs(&S[(r0 + i * RS) * CGH + cg]);
-    const float a = log_decay ? expf(log_decay[bh % H]) : 1.f;
+    const float2 a = decay_of(log_decay, bh % H);
     const float4 vv = la_load4(v + (size_t)bh * DV + 4 * cg);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
         const int r = r0 + i * RS;
         const float kc = to_f32(k[(size_t)bh * DK + r]), qc = to_f32(q[(size_t)bh * DK + r]);
-        s[i].x = fmaf(a, s[i].x, kc * vv.x); s[i].y = fmaf(a, s[i].y, kc * vv.y);
-        s[i].z = fmaf(a, s[i].z, kc * vv.z); s[i].w = fmaf(a, s[i].w, kc * vv.w);
+        s[i].x = fmaf(a.x, s[i].x, fmaf(a.y, s[i].x, kc * vv.x)); s[i].y = fmaf(a.x, s[i].y, fmaf(a.y, s[i].y, kc * vv.y));
+        s[i].z = fmaf(a.x, s[i].z, fmaf(a.y, s[i].z, kc * vv.z)); s[i].w = fmaf(a.x, s[i].w, fmaf(a.y, s[i].w, kc * vv.w));
         __stcs(&S[r * CGH + cg], s[i]);
         o.x += qc * s[i].x; o.y += qc * s[i].y; o.z += qc * s[i].z; o.w += qc * s[i].w;
     }
