@@ -672,10 +672,10 @@ paged_join_kernel(const __grid_constant__ PagedArgs a, unsigned int grid)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (c + i * kWarps >= count) break;         // what was loaded there is another share's
-            const float f = s_weight[c + i * kWarps];
+            const bool in = c + i * kWarps < count;     // else the last share's, which may be infinite
+            const float f = in ? s_weight[c + i * kWarps] : 0.f;
 #pragma unroll
-            for (int y = 0; y < DL; ++y) acc[y] += f * x[i][y];
+            for (int y = 0; y < DL; ++y) acc[y] += f * (in ? x[i][y] : 0.f);
         }
     }
 #pragma unroll
