@@ -591,8 +591,11 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
                 const int x0 = reread(sb + SM_TMEM + 4);
                 if (nown > 0) leave_state(a, x0, x0 / heads, me, flags, slots, S);
                 // The state that enters the segment: the contributions of all segments before it, or
-                // what segment 0 started from, one after the other through the q tiles.  Lane g holds
-                // how much fades over segment g.
+                // what segment 0 started from, one after the other through the q tiles, summed up from
+                // zero: the segment's own, which comes behind all of its outputs, may not be finite.
+                // Lane g holds how much fades over segment g.
+#pragma unroll
+                for (int i = 0; i < 64; ++i) S[i] = 0.f;
                 float wh = 0.f, wl = 0.f;
                 if (lane > 0 && lane < x0 / heads) {
                     int bh0, t0, t1;
