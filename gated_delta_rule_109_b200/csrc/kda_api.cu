@@ -21,6 +21,7 @@ kda_status cuda_fail(cudaError_t e)
 {
     snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "%s: %s",
              cudaGetErrorName(e), cudaGetErrorString(e));
+    cudaGetLastError();         // the runtime keeps it too: the next call's launch would report it
     return KDA_ERR_CUDA;
 }
 
