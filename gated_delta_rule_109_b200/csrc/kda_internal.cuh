@@ -111,18 +111,24 @@ void note_launch();
 
 // Sets a kernel's dynamic shared memory on the current device, the first time it is launched
 // there.  `done` is the call site's own: one flag per device, so that a later launch asks the
-// runtime for the device alone.
+// runtime for the device alone.  Only what succeeded is kept: after an error the next launch
+// asks again.  `registers`: the number per thread that the kernel counts on, where it does.
 struct OncePerDevice {
     std::atomic<bool> done[64];
 };
 template <typename Kernel>
-cudaError_t set_shared_memory(Kernel kernel, int bytes, OncePerDevice &once)
+cudaError_t set_shared_memory(Kernel kernel, int bytes, OncePerDevice &once, int registers = 0)
 {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const bool known = dev >= 0 && dev < 64;
     if (known && once.done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    if (registers) {
+        cudaFuncAttributes attr;
+        if ((e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess) return e;
+        if (attr.numRegs != registers) return cudaErrorInvalidKernelImage;
+    }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && known) once.done[dev].store(true, std::memory_order_release);
     return e;

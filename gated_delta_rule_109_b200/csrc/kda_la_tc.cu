@@ -36,7 +36,7 @@
 // as MN-major operand (tokens contracted) alike.
 #include <cuda.h>
 #include <cudaTypedefs.h>
-#include <mutex>
+#include <atomic>
 
 #include "kda_la.cuh"
 #include "kda_tc_ptx.cuh"
@@ -791,31 +791,27 @@ la_tc_kernel(const __grid_constant__ LaArgs a, const __grid_constant__ LaMaps ma
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tm));
 }
 
-// cuTensorMapEncodeTiled from the driver, looked up once (the library links the CUDA
-// runtime statically and not the driver library)
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
+// cuTensorMapEncodeTiled from the driver (the library links the CUDA runtime statically and not
+// the driver library), looked up until it has been found once
+cudaError_t map_encoder(PFN_cuTensorMapEncodeTiled_v12000 &fn)
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-        else
-            cudaGetLastError();
-    });
-    return fn;
+    static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+    if ((fn = found.load(std::memory_order_acquire))) return cudaSuccess;
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    found.store(fn, std::memory_order_release);
+    return cudaSuccess;
 }
 
 // A [B, T, H, 128] bf16 tensor as (channel, head, token, batch), boxes of one head's 64
 // channels x 128 tokens.  The token axis has its own bound: rows behind a sequence's end are
 // read as zeros and not written.
-cudaError_t token_map(const LaArgs &a, const void *p, CUtensorMap *m)
+cudaError_t token_map(PFN_cuTensorMapEncodeTiled_v12000 enc, const LaArgs &a, const void *p, CUtensorMap *m)
 {
-    const PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
-    if (!enc) return cudaErrorNotSupported;
     const cuuint64_t row = (cuuint64_t)a.H * kD * 2u;
     const cuuint64_t dims[4] = {(cuuint64_t)kD, (cuuint64_t)a.H, (cuuint64_t)a.T, (cuuint64_t)a.B};
     const cuuint64_t strides[3] = {(cuuint64_t)kD * 2u, row, row * (cuuint64_t)a.T};
@@ -825,12 +821,6 @@ cudaError_t token_map(const LaArgs &a, const void *p, CUtensorMap *m)
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-int launch_registers()
-{
-    cudaFuncAttributes attr;
-    return cudaFuncGetAttributes(&attr, la_tc_kernel) == cudaSuccess ? attr.numRegs : -1;
 }
 
 }  // namespace
@@ -844,20 +834,19 @@ size_t la_tc_workspace_bytes(const LaArgs &a)
 
 cudaError_t launch_la_tc(const LaArgs &a, cudaStream_t stream)
 {
+    static OncePerDevice once;
+    // the move of registers between warps is sized for this many: with fewer it would wait for ever
+    cudaError_t e = set_shared_memory(la_tc_kernel, (int)SM_TOTAL, once, kLaunchRegs);
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    if (e == cudaSuccess) e = map_encoder(enc);
     LaMaps maps;
-    cudaError_t e = cudaSuccess;
     for (int i = 0; i < a.npass && e == cudaSuccess; ++i) {
-        e = token_map(a, a.pass[i].q, &maps.q[i]);
-        if (e == cudaSuccess) e = token_map(a, a.pass[i].k, &maps.k[i]);
-        if (e == cudaSuccess) e = token_map(a, a.pass[i].v, &maps.v[i]);
-        if (e == cudaSuccess) e = token_map(a, a.pass[i].out, &maps.out[i]);
+        e = token_map(enc, a, a.pass[i].q, &maps.q[i]);
+        if (e == cudaSuccess) e = token_map(enc, a, a.pass[i].k, &maps.k[i]);
+        if (e == cudaSuccess) e = token_map(enc, a, a.pass[i].v, &maps.v[i]);
+        if (e == cudaSuccess) e = token_map(enc, a, a.pass[i].out, &maps.out[i]);
     }
     if (e != cudaSuccess) return e;
-    // the move of registers between warps is sized for this many: with fewer it would wait for ever
-    static const int regs = launch_registers();
-    if (regs != kLaunchRegs) return cudaErrorInvalidKernelImage;
-    static OncePerDevice once;
-    if ((e = set_shared_memory(la_tc_kernel, (int)SM_TOTAL, once)) != cudaSuccess) return e;
     int *flags = reinterpret_cast<int *>(a.ws);
     float *slots = nullptr;
     if (a.nseg > 1) {
