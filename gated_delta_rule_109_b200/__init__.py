@@ -717,6 +717,15 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
     return dict(dq=dq, dk=dkey, dv=dval, dinitial_state=ds0)
 
 
+def _dense(t: Optional[torch.Tensor]):
+    """t as the kernels take it, contiguous from a 16-byte boundary on: autograd hands over views
+    that need not be (the halves of a concatenation's gradient)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class LAFunction(torch.autograd.Function):
     """``out, final_state = LAFunction.apply(q, k, v, log_decay, initial_state)`` with
     ``kda_la_forward`` forward and ``kda_la_backward`` backward (once: no gradient of the
@@ -734,8 +743,7 @@ class LAFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_out, grad_final_state):
         q, k, v, log_decay, initial_state = ctx.saved_tensors
-        g = la_backward(q, k, v, log_decay, grad_out.contiguous(), initial_state,
-                        None if grad_final_state is None else grad_final_state.contiguous(),
+        g = la_backward(q, k, v, log_decay, _dense(grad_out), initial_state, _dense(grad_final_state),
                         initial_state_grad=initial_state is not None)
         return g["dq"], g["dk"], g["dv"], None, g["dinitial_state"]
 
