@@ -483,6 +483,15 @@ def backward(q, k, v, log_alpha, beta, grad_out, initial_state=None, grad_final_
     return g
 
 
+def _dense(t: Optional[torch.Tensor]):
+    """t as the kernels take it, contiguous from a 16-byte boundary on: autograd hands over views
+    that need not be (the halves of a concatenation's gradient)."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class KDAFunction(torch.autograd.Function):
     """``out, final_state = KDAFunction.apply(q, k, v, log_alpha, beta, initial_state)``
     with ``kda_forward`` forward and ``kda_backward`` backward (gradients in fp32,
@@ -497,8 +506,8 @@ class KDAFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_out, grad_final_state):
         q, k, v, log_alpha, beta, initial_state = ctx.saved_tensors
-        g = backward(q, k, v, log_alpha, beta, grad_out.contiguous().float(),
-                     initial_state, None if grad_final_state is None else grad_final_state.contiguous().float(),
+        g = backward(q, k, v, log_alpha, beta, _dense(grad_out.float()),
+                     initial_state, None if grad_final_state is None else _dense(grad_final_state.float()),
                      initial_state_grad=initial_state is not None)
         return (g["dq"].to(q.dtype), g["dk"].to(k.dtype), g["dv"].to(v.dtype), g["dlog_alpha"], g["dbeta"],
                 g["dinitial_state"])
@@ -715,15 +724,6 @@ def la_backward(q, k, v, log_decay, grad_out, initial_state=None, grad_final_sta
             _address(initial_state), grad_out.data_ptr(), _address(grad_final_state), dq.data_ptr(), dkey.data_ptr(),
             dval.data_ptr(), _address(ds0), B, T, H, dk, dv, code, scale)
     return dict(dq=dq, dk=dkey, dv=dval, dinitial_state=ds0)
-
-
-def _dense(t: Optional[torch.Tensor]):
-    """t as the kernels take it, contiguous from a 16-byte boundary on: autograd hands over views
-    that need not be (the halves of a concatenation's gradient)."""
-    if t is None:
-        return None
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 class LAFunction(torch.autograd.Function):
