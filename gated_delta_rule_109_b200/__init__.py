@@ -165,12 +165,15 @@ def _fits(t, shape, dtype, index) -> bool:
     return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
+def _code_of(dtype: torch.dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError("q, k, v must be bfloat16 or float32, got %s" % dtype)
+    return code
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
-        return KDA_BF16
-    if t.dtype == torch.float32:
-        return KDA_F32
-    raise TypeError("q, k, v must be bfloat16 or float32, got %s" % t.dtype)
+    return _code_of(t.dtype)
 
 
 def _need(t: torch.Tensor, name: str, shape, dtype=None, device=None):
@@ -646,7 +649,7 @@ def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, backward=False) ->
     """Bytes of the workspace of :func:`la_forward` (or :func:`la_backward`); 0: none is needed."""
     lib = load()
     fn = lib.kda_la_backward_workspace_bytes if backward else lib.kda_la_forward_workspace_bytes
-    return int(fn(int(B), int(T), int(H), int(dk), int(dv), KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+    return int(fn(int(B), int(T), int(H), int(dk), int(dv), _code_of(dtype)))
 
 
 def _need_la(q, k, v, log_decay, where, *more):
@@ -771,8 +774,7 @@ def la_decode_step(q, k, v, log_decay, state, *, out=None, scale: float = 0.0):
 
 def paged_decode_workspace_bytes(H: int, Hkv: int, D: int, dtype=torch.bfloat16) -> int:
     """Bytes of the workspace of :func:`paged_decode_step`, whatever the batch and lengths."""
-    return int(load().kda_paged_decode_workspace_bytes(int(H), int(Hkv), int(D),
-                                                       KDA_BF16 if dtype == torch.bfloat16 else KDA_F32))
+    return int(load().kda_paged_decode_workspace_bytes(int(H), int(Hkv), int(D), _code_of(dtype)))
 
 
 def paged_decode_step(q, k, v, k_cache, v_cache, block_table, lengths, *, out=None, scale: float = 0.0,
