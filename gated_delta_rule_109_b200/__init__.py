@@ -686,6 +686,8 @@ def la_forward(q, k, v, log_decay, initial_state=None, *, out=None, final_state=
     ``[B,T,H,dk]`` and v ``[B,T,H,dv]`` (bf16 or fp32, one dtype); log_decay ``[H]`` fp32
     (<= 0, a constant) or None (no decay); initial_state ``[B,H,dk,dv]`` fp32 or None.
     Returns ``(out [B,T,H,dv] in the dtype of q, final_state [B,H,dk,dv] fp32 or None)``.
+    The state is carried in fp32; bf16 with dk = dv = 128 rounds scores and entering states to
+    bf16 for their products, anything else rounds ``out`` alone (see kda.h).
     ``final_state`` may be ``initial_state`` (in-place carry).  ``scale`` 0 means
     1/sqrt(dk).  ``workspace``: a uint8 device tensor of at least
     :func:`la_workspace_bytes` bytes (allocated when None and needed).

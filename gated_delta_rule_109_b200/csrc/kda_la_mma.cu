@@ -416,14 +416,22 @@ cudaError_t launch_la_mma(const LaArgs &a, bool states_only, cudaStream_t stream
 // the walk is n times shorter, but every segment's own state has to be known first (a second
 // walk over k and v) and joined.  The number with the least modelled time is taken: waves of
 // CTAs x (chunks of a walk x the cost of both walks + a fixed cost of the join), in chunks of
-// the walk with outputs.
+// the walk with outputs.  The four costs were fitted to times in a graph; us, the number taken /
+// the best of 1 to 32 / one, forward:
+// bf16 128 x 128: B1 T1023 H8 30 / 27 / 30, B1 T4096 H16 43 / 43 / 93, B1 T8192 H4 49 / 47 / 169,
+// B1 T30000 H32 294 / 294 / 626, B1 T16384 H60 342 / 323 / 356, B4 T2047 H32 60 / 60 / 60;
+// fp32 128 x 128: B1 T1023 H8 45 / 43 / 264, B1 T30000 H32 2369 / 2369 / 7240; 64 x 64: B2 T1023 H8
+// 23 / 23 / 99, B1 T16384 H60 871 / 800 / 1649, B2 T5003 H90 863 / 712 / 862;
+// bf16 64 x 64: B1 T4096 H16 53 / 53 / 303; 128 x 64: B1 T16384 H60 1561 / 1560 / 2281.
+// Of 100 shapes, gradients among them, 4 are more than 1.1 off the best: the one of 712, the same in
+// bf16 (656 / 557), B1 T1023 H8 above, and the gradients of B1 T16384 H60 bf16 128 x 128 (959 / 775).
 void la_choose_segments(LaArgs &a)
 {
     constexpr int kMaxSegments = 32;        // a warp's lanes look at them
     const bool tc = la_tc_supported(a.dk, a.dv, a.dtype);
     const int C = tc ? 128 : kC;
     const int places = 148 * (!tc && a.dk == 64 && a.dv == 64 ? mma_resident<64, 64>() : 1);
-        const double state_cost = tc ? 0.6 : 0.5, join_cost = tc ? 3.0 : 1.0, per_segment = tc ? 0.5 : 0.05;
+    const double state_cost = tc ? 0.6 : 0.5, join_cost = tc ? 3.0 : 1.0, per_segment = tc ? 0.5 : 0.05;
     const int chunks = (a.T + C - 1) / C;
     const long long heads = (long long)a.npass * a.B * a.H;
     a.nseg = 1;

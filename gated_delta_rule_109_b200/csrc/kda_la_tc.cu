@@ -18,10 +18,11 @@
 // written as three bf16 parts that hold all 24 bits of the fp32 product, U starts afresh
 // every chunk (the tensor core's accumulation is short) and is added in registers, and
 // lambda^c is a pair of floats, because its rounding would grow with the number of chunks.
-// The third part is left out where it cannot be seen: two parts are off by at most 2^-17 of a
-// term, so they do for a state that only enters bf16 products, and for terms that fade to
-// less than 2^-6 of their size before the state is written out (their errors to 2^-23).  The
-// kernel runs into the power limit (1.5 of 1.97 GHz at B4 H32 T16384, 980 W), and U is half
+// The third part is left out where it is not seen: two parts are off by at most 2^-14.7 of a
+// term and 2^-17.7 in the root mean square (cut2), so they do for a state that only enters bf16
+// products, and for terms that fade to less than 2^-6 of their size before the state is written
+// out (their errors to 2^-20.7 and 2^-23.7; states measure 2e-7 off).  An output's last bit may
+// so depend on whether a final state is asked for.  The kernel runs into the power limit (1.5 of 1.97 GHz at B4 H32 T16384, 980 W), and U is half
 // of its products.
 //
 // Warps: 0-3 turn S into P and 4-7 rescale O and write the outputs (a thread is a token); 8-15
@@ -207,8 +208,10 @@ __device__ __forceinline__ float2 scale_pair(uint32_t k, float2 w)
 }
 // k w as the sum of two bf16, k a pair of bf16 and w = wh + wl in two parts, in packed bf16
 // arithmetic: hi = k wh rounded, whose error k wh - hi has at most 8 bits and is exact, and
-// mid = k wl + that error, rounded.  Off by at most 2^-17 of k w; half the instructions of the
-// same in fp32.
+// mid = k wl + that error, rounded.  mid is below 2^-6 of hi's power of two, so its rounding
+// costs up to 2^-15 of k w and the rest of w that wl does not hold 2^-17: off by at most 2^-14.7,
+// 2^-17.7 in the root mean square (over 2 10^7 random pairs: 2^-14.9 and 2^-17.75).  Half the
+// instructions of the same in fp32.
 __device__ __forceinline__ void cut2(uint32_t k, uint32_t wh, uint32_t wl, uint32_t &hi, uint32_t &mid)
 {
     asm("{\n\t.reg .b32 n;\n\tmul.rn.bf16x2 %0, %2, %3;\n\tneg.bf16x2 n, %0;\n\tfma.rn.bf16x2 n, %2, %3, n;\n\t"

@@ -6,7 +6,8 @@
 // moves its keys and values through its own ring of shared-memory slots with 16-byte
 // asynchronous copies, kStages - 1 units ahead, and looks the page of its next unit up one
 // unit before that.  Reading the cache is what bounds it: every key and value is read once
-// for all query heads of its group.
+// for the query heads of a block, which are all of its group's up to 16 (bf16) or 8 (fp32).  A
+// larger group has several blocks, and each reads the row again.
 //
 // bf16: the products are warp matrix instructions with the keys as rows, S^T = K q^T and
 // O^T = V^T P^T, so that the 8 columns are query heads and a group of fewer than 8 wastes
@@ -176,9 +177,13 @@ constexpr int resident() { return 226 * 1024 / (PagedSmem<D, InT, HG>::total + 1
 // few long ones the CTAs share the keys.  With `most` units in the longest row and `units` in
 // all, the first form takes about 6 us and a unit's time for every unit of every wave of CTAs, the
 // second 12 us, its share of the units, and 14 us for every row that begins in a CTA's share.
-// In a graph, us, shared / whole (32 / 8 heads of 128 bf16, rows up to L keys, drawn):
-// 64 rows, L 250 32 / 15, L 1000 53 / 37; 128 rows, L 450 64 / 33, L 5000 259 / 270;
-// 16 rows, L 450 19 / 17, L 2500 27 / 59; one row, L 500 11.5 / 16.2.
+// In a graph, us, shared / whole (rows up to L keys, drawn): 32 / 8 heads of 128 bf16: 40 rows, L 200
+// 21 / 13; 64 rows, L 1000 56 / 36; 128 rows, L 450 69 / 36, L 3000 173 / 166; 16 rows, L 450 19 / 17, L 2500
+// 38 / 56; one row, L 500 12 / 17.  32 / 1 heads of 64 bf16: 16 rows, L 450 15 / 12, L 2500 24 / 33.
+// 16 / 16 heads of 64 fp32: 24 rows, L 500 28 / 19; 16 rows, L 2500 57 / 70.  64 / 2 heads of 128
+// bf16, where the model is farthest off: 24 rows, L 500 35 / 29 (takes the first).  Over 97 such
+// shapes what the host picks is within 1.1 of the better form but for 5 (1.25 at most); with a wide
+// table, both forms with the second launch, the device's pick is within 1.1 but for 7 (1.28 at most).
 // (In hundredths of a us.)  `launched`: the kernel that joins has been launched, and costs 3 us even
 // if it finds nothing to do.
 template <int D, typename InT, int HG>

@@ -486,11 +486,20 @@ size_t kda_backward_workspace_bytes(int B, int T, int H, int dk, int dv);
  *                 sequence is cut so that few heads fill the device.  Not to be used by
  *                 another call that may run at the same time.
  *
- * Unlike kda_forward's, `out` has the dtype of q: the products of 16-bit inputs are
- * summed in fp32 and rounded once.  The state is fp32 throughout.  final_state may be
- * initial_state (in-place carry); any other overlap of inputs and outputs is undefined.
- * q and k need not be normalised.  Inputs are finite: an infinity or NaN in a token may
- * reach the outputs of earlier tokens of its chunk (128 tokens).
+ * Unlike kda_forward's, `out` has the dtype of q.  The state is carried in fp32 throughout,
+ * and sums are fp32.  What is rounded on the way to `out` depends on the form:
+ *   fp32, and bf16 with a head dimension of 64: products of fp32 operands, to 2^-22 of a
+ *     term; a bf16 out is rounded once, at the end.
+ *   bf16 with dk = dv = 128: as operands of their products the scores (with their decay) and
+ *     the state that enters a chunk are rounded to bf16, 2^-8 of each term at most, and out is
+ *     rounded at the end: 2.4e-3 of the outputs' norm, where that last rounding alone is
+ *     1.7e-3.  The errors are of the size of the terms, so they weigh more where the terms
+ *     cancel.  Whether a final state is asked for may change an output's last bit.
+ * The same holds for the gradients, with their own scores and states.
+ * final_state may be initial_state (in-place carry); any other overlap of inputs and outputs
+ * is undefined.  q and k need not be normalised.  Inputs are finite (in fp32 below
+ * (1 - 2^-12) 2^128): an infinity or NaN in a token may reach the outputs of earlier tokens
+ * of its chunk (128 tokens).
  *
  * Supported: dk, dv in {64, 128}, both dtypes; bf16 with dk = dv = 128 runs on the
  * tensor cores, anything else with fp32 operands in two parts each.  B, H >= 1, T >= 0; T = 0 writes no
@@ -535,7 +544,9 @@ size_t kda_la_backward_workspace_bytes(int B, int T, int H, int dk, int dv, kda_
  *   q, k [B, H, dk], v [B, H, dv], out [B, H, dv]  dtype; log_decay [H] float32 or NULL;
  *   state_inout [B, H, dk, dv] float32, read and overwritten.  Alignments as above.
  *
- * Equivalent to kda_la_forward with T = 1 and final_state == initial_state.
+ * Equivalent to kda_la_forward with T = 1 and final_state == initial_state, all in fp32, a
+ * bf16 out rounded once.  lambda is held to well below 2^-24; the fp32 state is rounded at
+ * every step, so a decay of less than 2^-25 may leave a state as it was.
  */
 kda_status kda_la_decode_step(const void *q, const void *k, const void *v, const float *log_decay,
                               float *state_inout, void *out, int B, int H, int dk, int dv,
