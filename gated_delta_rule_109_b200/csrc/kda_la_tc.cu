@@ -21,9 +21,10 @@
 // The third part is left out where it is not seen: two parts are off by at most 2^-14.7 of a
 // term and 2^-17.7 in the root mean square (cut2), so they do for a state that only enters bf16
 // products, and for terms that fade to less than 2^-6 of their size before the state is written
-// out (their errors to 2^-20.7 and 2^-23.7; states measure 2e-7 off).  An output's last bit may
-// so depend on whether a final state is asked for.  The kernel runs into the power limit (1.5 of 1.97 GHz at B4 H32 T16384, 980 W), and U is half
-// of its products.
+// out (their errors to 2^-20.7 and 2^-23.7; states measure 1e-7 to 6e-7 off, most of it what the
+// tensor core cuts off when it adds, towards zero).  An output's last bit may so depend on whether
+// a final state is asked for.  The kernel runs into the power limit (1.5 of 1.97 GHz at
+// B4 H32 T16384, 980 W), and U is half of its products.
 //
 // Warps: 0-3 turn S into P and 4-7 rescale O and write the outputs (a thread is a token); 8-15
 // make K'^T in tensor memory, groups of four by turns (ldmatrix transposes the K tile; while
